@@ -252,6 +252,125 @@ ola_status ola_decode_noalloc(const ola_geometry* geom, const float* S_ctx, cons
                               const void* k, const void* v, const float* g, const float* beta,
                               const int32_t* parent_idx, float* out_o, void* stream);
 
+/* ------------------------------------------------------ operators around the recurrence
+ * Not from the pages: what a layer runs before and beside its recurrence. The pages take q, k
+ * and v as given; a Gated DeltaNet layer makes them by a short causal convolution of its
+ * projections and a norm of every query and key head (ola_conv, ola_conv_step, ola_qk_norm).
+ * ola_scan and ola_scan_step are the recurrence of a selective state space layer: one scalar
+ * decay per head and token, the same state [d_v][d_k], no erase term.
+ *
+ * Conventions, beside those above:
+ * - Asynchronous on `stream`, no allocation, no host synchronisation: every call can be captured
+ *   into a CUDA graph. Outputs must not overlap inputs unless a function says so.
+ * - Strides are in elements, "tok" between consecutive tokens (or beams) and "seq" between
+ *   sequences; 0 stands for the contiguous value. Channels (heads x width) are contiguous.
+ *   A tok stride is at least the row's width; a sequence may not overlap the next one in outputs.
+ * - lens: device [R] int32 or NULL: sequence r has min(max(lens[r], 0), P) tokens and the rows
+ *   behind them are padding, never read into a result; the output rows there keep what they held.
+ * - parent_idx: device [R][B] int32 or NULL: beam b continues state parent_idx[r][b] of the Bp
+ *   states of its request. NULL: beam b continues state b (Bp = B) or the only one (Bp = 1). Out
+ *   of range: clamped to 0 and OLA_ERR_BAD_PARENT is recorded. A state may have many children.
+ * - Device-side errors (a bad parent, a bounded wait that ran out) go to one sticky word per
+ *   device; the call carries on. ola_layer_status reads and clears it.
+ * - Pointers to q, k, v, x, y, z and states: aligned to their element; 16-byte aligned pointers and
+ *   rows (strides) run on wide accesses and on tensor memory copies. fp32 pointers: 4 bytes. */
+
+/* Wait for `stream`, return the first device-side error that a call of this section recorded on
+ * the current device since the last ola_layer_status (OLA_OK if none), and clear it. Not to be
+ * called while `stream` is being captured. Errors: CUDA. */
+ola_status ola_layer_status(void* stream);
+
+/* Short depthwise causal convolution of W taps over u = state ++ x (the W-1 tokens before the
+ * sequence, zeros if state_in is NULL):
+ *   y[r][p][c] = act(bias[c] + sum_{i<W} w[c][i] u[r][p + i][c]),   act = identity or
+ *   SiLU(u) = u / (1 + exp(-u));  sums in fp32, y rounded once to in_dtype.
+ *   x         : [R][P][C] in_dtype (strides);  w : [C][W] fp32;  bias : [C] fp32 or NULL
+ *   state_in  : [R][W-1][C] in_dtype, oldest token first, or NULL;  may be state_out itself
+ *   y         : [R][P][C] in_dtype (strides);  y and x may be column slices of one wide buffer,
+ *               but not the same columns
+ *   state_out : [R][W-1][C] in_dtype or NULL: the last W-1 tokens of u up to the sequence's end
+ * R >= 1, P >= 0 (P = 0: state_out = state_in), C >= 1, W 2..4.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+typedef struct {
+  int32_t R, P, C, W;
+  int32_t in_dtype;               /* OLA_F32 or OLA_BF16 */
+  int32_t silu;                   /* 1: SiLU, 0: identity */
+  int64_t x_tok, x_seq, y_tok, y_seq;
+} ola_conv_desc;
+ola_status ola_conv(const ola_conv_desc* d, const void* x, const float* w, const float* bias,
+                    const void* state_in, const int32_t* lens, void* y, void* state_out,
+                    void* stream);
+
+/* ola_conv for one token of each of B = d->P beams per request:
+ *   x, y [R][B][C];  state_in [R][Bp][W-1][C];  state_out [R][B][W-1][C] (required): the parent's
+ *   window without its oldest token, then x. state_out may be state_in itself if parent_idx is
+ *   NULL and Bp = B. The window of beam b after a step is thus the last W-1 tokens of its chain.
+ * B >= 1, Bp >= 1. Errors as ola_conv. */
+ola_status ola_conv_step(const ola_conv_desc* d, int32_t Bp, const void* x, const float* w,
+                         const float* bias, const void* state_in, const int32_t* parent_idx,
+                         void* y, void* state_out, void* stream);
+
+/* Norm of every query and key head, then the position rotation, in one pass:
+ *   n = x * rsqrt(m + eps) (* w[i]),   m = mean of x^2 over the head, or (l2) their sum
+ *   pairs (a, b) of the first `rot` dims: (a cos - b sin, b cos + a sin) with the angle
+ *   pos * inv_freq[i] taken in fp64, i the pair's index; pairs are (i, i + rot/2), or with
+ *   `pair` (2i, 2i + 1). Norm and rotation in fp32, rounded once to in_dtype.
+ *   q [N][Hq][d], k [N][Hk][d] in_dtype with N tokens (q_tok, k_tok: strides); q_out, k_out the
+ *   same with strides qo_tok, ko_tok; q_out may be q itself (same stride), k_out may be k.
+ *   wq, wk : [d] fp32 or NULL;  positions : [N] int32;  inv_freq : [rot/2] fp32 (both may be
+ *   NULL if rot = 0)
+ * N >= 0, Hq >= 0, Hk >= 0 (q, q_out may be NULL if Hq = 0; so k), d a multiple of 8 up to 512,
+ * rot a multiple of 16 up to d, eps >= 0, pointers and strides 16-byte aligned (wq, wk, positions
+ * and inv_freq 4). eps = 0 gives NaN for an all-zero head, as the formula does. A non-finite
+ * value stays within its head. Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+typedef struct {
+  int64_t N;
+  int32_t Hq, Hk, d;
+  int32_t in_dtype;
+  int32_t l2;                     /* 1: sum of squares, 0: mean of squares */
+  int32_t rot;                    /* rotated dims, 0 = none */
+  int32_t pair;                   /* 1: pairs (2i, 2i + 1), 0: (i, i + rot/2) */
+  float eps;
+  int64_t q_tok, k_tok, qo_tok, ko_tok;
+} ola_qk_desc;
+ola_status ola_qk_norm(const ola_qk_desc* d, const void* q, const void* k, const float* wq,
+                       const float* wk, const int32_t* positions, const float* inv_freq,
+                       void* q_out, void* k_out, void* stream);
+
+/* Selective state space scan of a prompt: for each sequence r and head h, with the key group
+ * g = h / (H / G), from S = S_in (zeros if NULL), token by token
+ *   dt = softplus(dt[r][p][h] + dt_bias[h])  (softplus = 0: dt as given, plus dt_bias)
+ *   S <- exp(dt A[h]) S + dt v k^T,   o = S q + D[h] v,   y = o * SiLU(z)   (z, D if given)
+ *   v, z, y : [R][P][H][d_v] in_dtype (strides);  k, q : [R][P][G][d_k] in_dtype (strides)
+ *   dt      : [R][P][H] fp32;  A, D, dt_bias : [H] fp32, D and dt_bias may be NULL
+ *   S_in    : [R][H][d_v][d_k] fp32 or NULL;  S_out : the same, or NULL; may be S_in itself
+ *   ws      : device scratch of ola_scan_workspace_bytes(d) bytes, 16-byte aligned (NULL if 0).
+ *             Calls that may overlap on the GPU need scratch of their own.
+ * d_k, d_v in {16, 32, 64, 128, 256}, G divides H, P >= 0. dt * A is taken to be <= 0 (a decay);
+ * growth is computed as the formula says as long as it does not overflow. States and sums are
+ * fp32, token by token. Long prompts of few sequences are cut into pieces that run side by side and
+ * are joined through `ws`. Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+typedef struct {
+  int32_t R, P, H, G, d_k, d_v;
+  int32_t in_dtype;
+  int32_t softplus;
+  int64_t v_tok, v_seq, k_tok, k_seq, q_tok, q_seq, z_tok, z_seq, y_tok, y_seq;
+} ola_scan_desc;
+ola_status ola_scan_workspace_bytes(const ola_scan_desc* d, uint64_t* out_bytes);
+ola_status ola_scan(const ola_scan_desc* d, const void* v, const float* dt, const float* A,
+                    const void* k, const void* q, const float* D, const float* dt_bias,
+                    const void* z, const float* S_in, const int32_t* lens, void* y, float* S_out,
+                    void* ws, uint64_t ws_bytes, void* stream);
+
+/* ola_scan for one token of each of B = d->P beams per request: v, z, y [R][B][H][d_v],
+ * k, q [R][B][G][d_k], dt [R][B][H], state_in [R][Bp][H][d_v][d_k] fp32, state_out
+ * [R][B][H][d_v][d_k] fp32 (required; state_in itself if parent_idx is NULL and Bp = B).
+ * States 16-byte aligned. Token by token in fp32. Errors as ola_scan. */
+ola_status ola_scan_step(const ola_scan_desc* d, int32_t Bp, const void* v, const float* dt,
+                         const float* A, const void* k, const void* q, const float* D,
+                         const float* dt_bias, const void* z, const float* state_in,
+                         const int32_t* parent_idx, void* y, float* state_out, void* stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif

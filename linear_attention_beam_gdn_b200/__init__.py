@@ -18,7 +18,9 @@ from typing import Optional
 __all__ = ["OlaError", "LibraryMissing", "Geometry", "lib", "Decoder", "prefill",
            "OLA_F32", "OLA_BF16", "OLA_PATH_REPLAY", "OLA_PATH_FULLSTATE", "OLA_PATH_REPLAYSSM",
            "OLA_MATH_FP32",
-           "OLA_MATH_TENSOR", "LIB_PATH", "HEADER_PATH", "declared_symbols"]
+           "OLA_MATH_TENSOR", "LIB_PATH", "HEADER_PATH", "declared_symbols",
+           "ConvDesc", "QkDesc", "ScanDesc", "conv", "conv_step", "qk_norm", "scan", "scan_step",
+           "layer_status"]
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "_build", "libola.so")
@@ -51,6 +53,25 @@ class Geometry(ctypes.Structure):
                 ("math", ctypes.c_int32)]
 
 
+class ConvDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("R", "P", "C", "W", "in_dtype", "silu")] +
+                [(n, ctypes.c_int64) for n in ("x_tok", "x_seq", "y_tok", "y_seq")])
+
+
+class QkDesc(ctypes.Structure):
+    _fields_ = ([("N", ctypes.c_int64)] +
+                [(n, ctypes.c_int32) for n in ("Hq", "Hk", "d", "in_dtype", "l2", "rot", "pair")] +
+                [("eps", ctypes.c_float)] +
+                [(n, ctypes.c_int64) for n in ("q_tok", "k_tok", "qo_tok", "ko_tok")])
+
+
+class ScanDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("R", "P", "H", "G", "d_k", "d_v", "in_dtype",
+                                               "softplus")] +
+                [(n, ctypes.c_int64) for n in ("v_tok", "v_seq", "k_tok", "k_seq", "q_tok",
+                                               "q_seq", "z_tok", "z_seq", "y_tok", "y_seq")])
+
+
 _LIB: Optional[ctypes.CDLL] = None
 _P = ctypes.c_void_p
 
@@ -73,6 +94,13 @@ def _declare(L: ctypes.CDLL) -> None:
         "ola_compact": (i32, [_P, ctypes.POINTER(ctypes.c_int32), _P]),
         "ola_destroy": (i32, [_P]),
         "ola_prefill": (i32, [i32, i32, i32, i32, i32, i32, _P, _P, _P, _P, _P, _P]),
+        "ola_layer_status": (i32, [_P]),
+        "ola_conv": (i32, [ctypes.POINTER(ConvDesc)] + [_P] * 8),
+        "ola_conv_step": (i32, [ctypes.POINTER(ConvDesc), i32] + [_P] * 8),
+        "ola_qk_norm": (i32, [ctypes.POINTER(QkDesc)] + [_P] * 9),
+        "ola_scan_workspace_bytes": (i32, [ctypes.POINTER(ScanDesc), u64p]),
+        "ola_scan": (i32, [ctypes.POINTER(ScanDesc)] + [_P] * 13 + [ctypes.c_uint64, _P]),
+        "ola_scan_step": (i32, [ctypes.POINTER(ScanDesc), i32] + [_P] * 13),
         "ola_noalloc_scratch_bytes": (ctypes.c_uint64, [ctypes.POINTER(Geometry)]),
         "ola_decode_noalloc": (i32, [ctypes.POINTER(Geometry), _P, _P, _P, _P, _P, _P, _P, _P,
                                      _P]),
@@ -188,6 +216,44 @@ def ola_decode_noalloc(geom: Geometry, S_ctx, q, k, v, g, beta, parent_idx, out_
                        stream) -> int:
     return lib().ola_decode_noalloc(ctypes.byref(geom), S_ctx, q, k, v, g, beta, parent_idx,
                                     out_o, stream)
+
+
+def ola_layer_status(stream) -> int:
+    return lib().ola_layer_status(stream)
+
+
+def ola_conv(desc: ConvDesc, x, w, bias, state_in, lens, y, state_out, stream) -> int:
+    return lib().ola_conv(ctypes.byref(desc), x, w, bias, state_in, lens, y, state_out, stream)
+
+
+def ola_conv_step(desc: ConvDesc, Bp, x, w, bias, state_in, parent_idx, y, state_out,
+                  stream) -> int:
+    return lib().ola_conv_step(ctypes.byref(desc), Bp, x, w, bias, state_in, parent_idx, y,
+                               state_out, stream)
+
+
+def ola_qk_norm(desc: QkDesc, q, k, wq, wk, positions, inv_freq, q_out, k_out, stream) -> int:
+    return lib().ola_qk_norm(ctypes.byref(desc), q, k, wq, wk, positions, inv_freq, q_out, k_out,
+                             stream)
+
+
+def ola_scan_workspace_bytes(desc: ScanDesc) -> int:
+    out = ctypes.c_uint64(0)
+    _check(lib().ola_scan_workspace_bytes(ctypes.byref(desc), ctypes.byref(out)),
+           "ola_scan_workspace_bytes")
+    return out.value
+
+
+def ola_scan(desc: ScanDesc, v, dt, A, k, q, D, dt_bias, z, S_in, lens, y, S_out, ws, ws_bytes,
+             stream) -> int:
+    return lib().ola_scan(ctypes.byref(desc), v, dt, A, k, q, D, dt_bias, z, S_in, lens, y, S_out,
+                          ws, ws_bytes, stream)
+
+
+def ola_scan_step(desc: ScanDesc, Bp, v, dt, A, k, q, D, dt_bias, z, state_in, parent_idx, y,
+                  state_out, stream) -> int:
+    return lib().ola_scan_step(ctypes.byref(desc), Bp, v, dt, A, k, q, D, dt_bias, z, state_in,
+                               parent_idx, y, state_out, stream)
 
 
 # ------------------------------------------------------------------ torch-facing wrappers
@@ -370,3 +436,279 @@ class Decoder:
 
     def __exit__(self, *exc):
         self.close()
+
+
+# ------------------------------------------------------------------ operators around the recurrence
+#
+# Each call runs on the device of its first tensor and on `stream` (default: that device's current
+# stream), allocates only the outputs and scratch that it is not given (they belong to that
+# stream), and does not wait. Inputs
+# that may be strided are [sequence, token, ...] with contiguous channels, so a slice of a wide
+# projection's columns is taken as it is.
+
+def _on(x, name, shape, dtype, device, strided=False):
+    """Checks a tensor argument of an operator; returns its pointer."""
+    if not strided:
+        return _need(x, shape, dtype, name, device)
+    torch = _torch()
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.device != device:
+        raise ValueError(f"{name} is on {x.device}, expected {device}")
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
+    if x.dtype != dtype:
+        raise TypeError(f"{name} has dtype {x.dtype}, expected {dtype}")
+    width, inner = 1, True
+    for n, s in zip(reversed(x.shape[2:]), reversed(x.stride()[2:])):
+        inner = inner and (n == 1 or s == width)
+        width *= n
+    R, P = x.shape[:2]
+    if not inner or (P > 1 and x.stride(1) < width) or (R > 1 and x.stride(0) < 1):
+        raise ValueError(f"{name}: channels must be contiguous and tokens must not overlap")
+    return x.data_ptr()
+
+
+def _strides(x):
+    """(token, sequence) strides in elements; 0 (contiguous) where the extent is 1."""
+    return (x.stride(1) if x.shape[1] > 1 else 0), (x.stride(0) if x.shape[0] > 1 else 0)
+
+
+def _tok_strides(x):
+    """The same, with the token stride of a single token made explicit."""
+    tok, seq = _strides(x)
+    width = 1
+    for n in x.shape[2:]:
+        width *= n
+    return tok or width, seq or max(1, x.shape[1]) * (tok or width)
+
+
+def _first(x, name, ndim):
+    torch = _torch()
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.device.type != "cuda":
+        raise ValueError(f"{name} must be on a CUDA device")
+    if x.dim() != ndim:
+        raise ValueError(f"{name} has {x.dim()} dimensions, expected {ndim}")
+    _dtype_code(x.dtype)
+    return x.device
+
+
+class _Scope:
+    """The device of a call and the stream its kernels and allocations belong to."""
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        self.device = torch.cuda.device(device)
+        self.stream = torch.cuda.stream(stream) if stream is not None else None
+
+    def __enter__(self):
+        self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        self.device.__exit__(*exc)
+
+
+def _opt(x, name, shape, dtype, device, strided=False):
+    return None if x is None else _on(x, name, shape, dtype, device, strided)
+
+
+def layer_status(device=None, stream=None) -> int:
+    """Waits for `stream` and returns the first device-side error that an operator recorded on
+    `device` (default: the current one) since the last call (OLA_OK if none), and clears it."""
+    torch = _torch()
+    with torch.cuda.device(device):
+        st = ola_layer_status(_stream_ptr(stream))
+    if st in (OLA_ERR_CUDA, OLA_ERR_UNSUPPORTED):
+        raise OlaError(st, "ola_layer_status")
+    return st
+
+
+def conv(x, w, bias=None, *, state=None, lens=None, silu=True, out=None, state_out=None,
+         stream=None):
+    """Short causal convolution of a prompt (ola_conv): x [R, P, C] (bf16 or fp32, may be a column
+    slice), w [C, W] and bias [C] fp32, state [R, W-1, C] (the tokens before, default zeros), lens
+    [R] int32 for a padded batch. Returns (y [R, P, C], state_out [R, W-1, C]); rows of `out`
+    behind a sequence's end are not written. state_out may be `state`."""
+    torch = _torch()
+    dev = _first(x, "x", 3)
+    R, P, C = x.shape
+    if w.dim() != 2:
+        raise ValueError("w must be [C, W]")
+    W = w.shape[1]
+    dt = x.dtype
+    with _Scope(dev, stream):
+        if out is None:
+            out = torch.empty((R, P, C), device=dev, dtype=dt)
+        if state_out is None:
+            state_out = torch.empty((R, max(W - 1, 0), C), device=dev, dtype=dt)
+        args = [_on(x, "x", (R, P, C), dt, dev, True), _on(w, "w", (C, W), torch.float32, dev),
+                _opt(bias, "bias", (C,), torch.float32, dev),
+                _opt(state, "state", (R, W - 1, C), dt, dev),
+                _opt(lens, "lens", (R,), torch.int32, dev),
+                _on(out, "out", (R, P, C), dt, dev, True),
+                _on(state_out, "state_out", (R, W - 1, C), dt, dev)]
+        d = ConvDesc(R, P, C, W, _dtype_code(dt), int(bool(silu)), *_tok_strides(x),
+                     *_tok_strides(out))
+        _check(ola_conv(d, *args, _stream_ptr(stream)), "ola_conv")
+    return out, state_out
+
+
+def conv_step(x, w, bias=None, *, state, parent_idx=None, silu=True, out=None, state_out=None,
+              stream=None):
+    """One token of every beam through the convolution (ola_conv_step): x [R, B, C], state
+    [R, Bp, W-1, C], parent_idx [R, B] int32 (default: beam b continues state b, or the only
+    one). Returns (y [R, B, C], state_out [R, B, W-1, C]); state_out may be `state` when
+    parent_idx is None."""
+    torch = _torch()
+    dev = _first(x, "x", 3)
+    R, B, C = x.shape
+    if w.dim() != 2:
+        raise ValueError("w must be [C, W]")
+    if state.dim() != 4:
+        raise ValueError("state must be [R, Bp, W-1, C]")
+    W, Bp, dt = w.shape[1], state.shape[1], x.dtype
+    with _Scope(dev, stream):
+        if out is None:
+            out = torch.empty((R, B, C), device=dev, dtype=dt)
+        if state_out is None:
+            state_out = torch.empty((R, B, max(W - 1, 0), C), device=dev, dtype=dt)
+        args = [_on(x, "x", (R, B, C), dt, dev, True), _on(w, "w", (C, W), torch.float32, dev),
+                _opt(bias, "bias", (C,), torch.float32, dev),
+                _on(state, "state", (R, Bp, W - 1, C), dt, dev),
+                _opt(parent_idx, "parent_idx", (R, B), torch.int32, dev),
+                _on(out, "out", (R, B, C), dt, dev, True),
+                _on(state_out, "state_out", (R, B, W - 1, C), dt, dev)]
+        d = ConvDesc(R, B, C, W, _dtype_code(dt), int(bool(silu)), *_tok_strides(x),
+                     *_tok_strides(out))
+        _check(ola_conv_step(d, Bp, *args, _stream_ptr(stream)), "ola_conv_step")
+    return out, state_out
+
+
+def _tokens(x, name, device, dtype):
+    """(pointer, N, token stride) of a tensor [R, P, H, d] whose tokens are evenly spaced."""
+    R, P, H, d = x.shape
+    ptr = _on(x, name, (R, P, H, d), dtype, device, True)
+    tok, seq = _tok_strides(x)
+    if P == 1:
+        tok = seq if R > 1 else tok
+    elif R > 1 and seq != P * tok:
+        raise ValueError(f"{name}: sequences must follow one another at the token stride")
+    return ptr, R * P, tok
+
+
+def qk_norm(q, k, *, wq=None, wk=None, eps=1e-6, l2=False, positions=None, inv_freq=None,
+            pair=False, q_out=None, k_out=None, stream=None):
+    """Norm of every query and key head and the position rotation in one pass (ola_qk_norm):
+    q [R, P, Hq, d], k [R, P, Hk, d] (may be column slices of one projection), weights [d] fp32,
+    l2=True for unit heads instead of unit mean square; with inv_freq [rot/2] fp32 and positions
+    [R, P] int32 the first `rot` dims are rotated, pairs (i, i + rot/2) or (pair=True)
+    (2i, 2i + 1). Returns (q_out, k_out); q_out may be q and k_out may be k."""
+    torch = _torch()
+    dev = _first(q, "q", 4)
+    if k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3]:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected [R, P, Hk, d] as q's")
+    R, P, Hq, d = q.shape
+    Hk, dt = k.shape[2], q.dtype
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq go together")
+    rot = 2 * inv_freq.numel() if inv_freq is not None else 0
+    with _Scope(dev, stream):
+        if q_out is None:
+            q_out = torch.empty((R, P, Hq, d), device=dev, dtype=dt)
+        if k_out is None:
+            k_out = torch.empty((R, P, Hk, d), device=dev, dtype=dt)
+        if tuple(q_out.shape) != tuple(q.shape) or tuple(k_out.shape) != tuple(k.shape):
+            raise ValueError("q_out and k_out must have the shapes of q and k")
+        qp, N, q_tok = _tokens(q, "q", dev, dt)
+        kp, _, k_tok = _tokens(k, "k", dev, dt)
+        qo, _, qo_tok = _tokens(q_out, "q_out", dev, dt)
+        ko, _, ko_tok = _tokens(k_out, "k_out", dev, dt)
+        args = [qp, kp, _opt(wq, "wq", (d,), torch.float32, dev),
+                _opt(wk, "wk", (d,), torch.float32, dev),
+                _opt(positions, "positions", (R, P), torch.int32, dev),
+                _opt(inv_freq, "inv_freq", (rot // 2,), torch.float32, dev), qo, ko]
+        desc = QkDesc(N, Hq, Hk, d, _dtype_code(dt), int(bool(l2)), rot, int(bool(pair)), eps,
+                      q_tok, k_tok, qo_tok, ko_tok)
+        _check(ola_qk_norm(desc, *args, _stream_ptr(stream)), "ola_qk_norm")
+    return q_out, k_out
+
+
+def _scan_common(v, dt, A, k, q, D, dt_bias, z, out, softplus, dev):
+    torch = _torch()
+    f32 = torch.float32
+    R, P, H, d_v = v.shape
+    if k.dim() != 4:
+        raise ValueError("k must be [R, P, G, d_k]")
+    G, d_k, t = k.shape[2], k.shape[3], v.dtype
+    ptrs = dict(v=_on(v, "v", (R, P, H, d_v), t, dev, True),
+                dt=_on(dt, "dt", (R, P, H), f32, dev), A=_on(A, "A", (H,), f32, dev),
+                k=_on(k, "k", (R, P, G, d_k), t, dev, True),
+                q=_on(q, "q", (R, P, G, d_k), t, dev, True),
+                D=_opt(D, "D", (H,), f32, dev), dt_bias=_opt(dt_bias, "dt_bias", (H,), f32, dev),
+                z=_opt(z, "z", (R, P, H, d_v), t, dev, True),
+                y=_on(out, "out", (R, P, H, d_v), t, dev, True))
+    desc = ScanDesc(R, P, H, G, d_k, d_v, _dtype_code(t), int(bool(softplus)), *_tok_strides(v),
+                    *_tok_strides(k), *_tok_strides(q),
+                    *(_tok_strides(z) if z is not None else (0, 0)), *_tok_strides(out))
+    return desc, ptrs
+
+
+def scan(v, dt, A, k, q, *, D=None, dt_bias=None, z=None, S_in=None, lens=None, softplus=True,
+         out=None, S_out=None, stream=None):
+    """Selective state space scan of a prompt (ola_scan): v [R, P, H, d_v], k, q [R, P, G, d_k]
+    (bf16 or fp32, may be column slices), dt [R, P, H] fp32, A [H] fp32 (negative), optional D,
+    dt_bias [H] fp32, gate z like v, S_in [R, H, d_v, d_k] fp32, lens [R] int32.
+    Returns (y [R, P, H, d_v], S_out [R, H, d_v, d_k]); rows of `out` behind a sequence's end are
+    not written. S_out may be S_in."""
+    torch = _torch()
+    dev = _first(v, "v", 4)
+    R, P, H, d_v = v.shape
+    with _Scope(dev, stream):
+        if out is None:
+            out = torch.empty((R, P, H, d_v), device=dev, dtype=v.dtype)
+        desc, p = _scan_common(v, dt, A, k, q, D, dt_bias, z, out, softplus, dev)
+        shape = (R, H, d_v, desc.d_k)
+        if S_out is None:
+            S_out = torch.empty(shape, device=dev, dtype=torch.float32)
+        s_in = _opt(S_in, "S_in", shape, torch.float32, dev)
+        s_out = _on(S_out, "S_out", shape, torch.float32, dev)
+        len_p = _opt(lens, "lens", (R,), torch.int32, dev)
+        n = ola_scan_workspace_bytes(desc)
+        ws = torch.empty((n,), device=dev, dtype=torch.uint8) if n else None
+        _check(ola_scan(desc, p["v"], p["dt"], p["A"], p["k"], p["q"], p["D"], p["dt_bias"],
+                        p["z"], s_in, len_p, p["y"], s_out, ws.data_ptr() if n else None, n,
+                        _stream_ptr(stream)), "ola_scan")
+    return out, S_out
+
+
+def scan_step(v, dt, A, k, q, *, state, D=None, dt_bias=None, z=None, parent_idx=None,
+              softplus=True, out=None, state_out=None, stream=None):
+    """One token of every beam through the scan (ola_scan_step): v [R, B, H, d_v], k, q
+    [R, B, G, d_k], dt [R, B, H], state [R, Bp, H, d_v, d_k] fp32, parent_idx [R, B] int32
+    (default: beam b continues state b, or the only one). Returns (y [R, B, H, d_v], state_out
+    [R, B, H, d_v, d_k]); state_out may be `state` when parent_idx is None."""
+    torch = _torch()
+    dev = _first(v, "v", 4)
+    R, B, H, d_v = v.shape
+    if state.dim() != 5:
+        raise ValueError("state must be [R, Bp, H, d_v, d_k]")
+    Bp = state.shape[1]
+    with _Scope(dev, stream):
+        if out is None:
+            out = torch.empty((R, B, H, d_v), device=dev, dtype=v.dtype)
+        desc, p = _scan_common(v, dt, A, k, q, D, dt_bias, z, out, softplus, dev)
+        if state_out is None:
+            state_out = torch.empty((R, B, H, d_v, desc.d_k), device=dev, dtype=torch.float32)
+        s_in = _on(state, "state", (R, Bp, H, d_v, desc.d_k), torch.float32, dev)
+        s_out = _on(state_out, "state_out", (R, B, H, d_v, desc.d_k), torch.float32, dev)
+        par = _opt(parent_idx, "parent_idx", (R, B), torch.int32, dev)
+        _check(ola_scan_step(desc, Bp, p["v"], p["dt"], p["A"], p["k"], p["q"], p["D"],
+                             p["dt_bias"], p["z"], s_in, par, p["y"], s_out,
+                             _stream_ptr(stream)), "ola_scan_step")
+    return out, state_out

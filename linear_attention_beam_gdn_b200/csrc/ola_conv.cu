@@ -1,0 +1,223 @@
+// Short depthwise causal convolution, for prompts and for one token of every beam.
+//
+//     y[p][c] = act(bias[c] + sum_{i<W} w[c][i] u[p + i][c]),   u = (W-1 earlier tokens) ++ x
+//
+// 2W + a few operations per element against one read and one write of it: the bound is HBM. A
+// thread owns 16 bytes of neighbouring channels, keeps their W taps in registers and walks
+// consecutive tokens with the window of the last W-1 inputs in registers, so an element is read
+// once (plus the W-1 tokens before each thread's stretch, which its neighbour's reads leave in
+// L2). The window's values are moved, never recomputed: the state that leaves is the input's bits.
+#include "ola_layer.cuh"
+
+namespace ola {
+
+namespace {
+
+constexpr int kConvThreads = 128;
+constexpr int kConvUnroll = 4;      // tokens loaded together
+
+template <typename T, int VEC, int W>
+struct Taps {
+  float w[W][VEC], b[VEC];
+  __device__ __forceinline__ void load(const ConvArgs& a, int c) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i][e] = __ldg(a.w + size_t(c + e) * W + i);
+      b[e] = a.bias ? __ldg(a.bias + c + e) : 0.f;
+    }
+  }
+  // win[0..W-2] the earlier tokens, oldest first, x the newest
+  __device__ __forceinline__ void apply(const float (&win)[W - 1][VEC], const float (&x)[VEC],
+                                        int silu, float (&y)[VEC]) const {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      float u = b[e];
+#pragma unroll
+      for (int i = 0; i < W - 1; ++i) u = fmaf(w[i][e], win[i][e], u);
+      u = fmaf(w[W - 1][e], x[e], u);
+      y[e] = silu ? silu_f<T>(u) : u;
+    }
+  }
+};
+
+// blockDim = (channel vectors, token stretches); grid.x = channel blocks x token blocks x R.
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvArgs a) {
+  const int ct = blockIdx.x % a.n_ctile;
+  const int rest = blockIdx.x / a.n_ctile;
+  const int r = rest / a.n_ttile;
+  const int64_t tile = int64_t(rest % a.n_ttile) * blockDim.y + threadIdx.y;
+  const int c = (ct * blockDim.x + threadIdx.x) * VEC;
+  const int64_t t0w = tile * a.tt;
+  if (c >= a.C || (t0w >= a.P && tile > 0)) return;
+  const int t0 = int(t0w);
+  const int L = seq_len(a.lens, r, a.P);
+  const int t1 = min(t0 + a.tt, L);
+  const T* x = static_cast<const T*>(a.x) + int64_t(r) * a.x_seq + c;
+  T* y = static_cast<T*>(a.y) + int64_t(r) * a.y_seq + c;
+  // the window before the stretch: earlier tokens, or the incoming state
+  const T* si = a.state_in
+                    ? static_cast<const T*>(a.state_in) + int64_t(r) * (W - 1) * a.C + c
+                    : nullptr;
+  float win[W - 1][VEC];
+  if (t0 == 0) {
+    Pack<T, VEC> keep[W - 1];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      keep[j].zero();
+      if (si) keep[j].load(si + int64_t(j) * a.C);
+      keep[j].unpack(win[j]);
+    }
+    if (a.state_out) {
+      // the last W-1 tokens of state ++ x[:L]; every read precedes the first write, so that
+      // state_out may be state_in (no other thread touches these channels' states)
+      Pack<T, VEC> out[W - 1];
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) {
+        const int t = L + j - (W - 1);
+        if (t >= 0) {
+          out[j].load(x + int64_t(t) * a.x_tok);
+        } else {
+#pragma unroll
+          for (int i = 0; i < W - 1; ++i)
+            if (i == t + W - 1) out[j] = keep[i];
+        }
+      }
+      T* so = static_cast<T*>(a.state_out) + int64_t(r) * (W - 1) * a.C + c;
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) out[j].store(so + int64_t(j) * a.C);
+    }
+    if (t1 <= 0) return;
+  } else {
+    if (t0 >= t1) return;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {             // tt >= W - 1: these tokens exist
+      Pack<T, VEC> p;
+      p.load(x + int64_t(t0 + j - (W - 1)) * a.x_tok);
+      p.unpack(win[j]);
+    }
+  }
+  Taps<T, VEC, W> taps;
+  taps.load(a, c);
+  for (int t = t0; t < t1; t += kConvUnroll) {
+    Pack<T, VEC> in[kConvUnroll];
+#pragma unroll
+    for (int i = 0; i < kConvUnroll; ++i) {
+      in[i].zero();
+      if (t + i < t1) in[i].load(x + int64_t(t + i) * a.x_tok);
+    }
+#pragma unroll
+    for (int i = 0; i < kConvUnroll; ++i) {
+      if (t + i >= t1) break;
+      float xf[VEC], yf[VEC];
+      in[i].unpack(xf);
+      taps.apply(win, xf, a.silu, yf);
+      Pack<T, VEC> o;
+      o.pack(yf);
+      o.store(y + int64_t(t + i) * a.y_tok);
+#pragma unroll
+      for (int j = 0; j < W - 2; ++j) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) win[W - 2][e] = xf[e];
+    }
+  }
+}
+
+// One token of every beam: thread = 16 bytes of channels x tt consecutive beams (of all requests).
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvArgs a) {
+  const int ct = blockIdx.x % a.n_ctile;
+  const int64_t tile = int64_t(blockIdx.x / a.n_ctile) * blockDim.y + threadIdx.y;
+  const int c = (ct * blockDim.x + threadIdx.x) * VEC;
+  const int64_t n = int64_t(a.R) * a.P;
+  const int64_t i0 = tile * a.tt, i1 = min(i0 + a.tt, n);
+  if (c >= a.C || i0 >= i1) return;
+  Taps<T, VEC, W> taps;
+  taps.load(a, c);
+  for (int64_t i = i0; i < i1; ++i) {
+    const int r = int(i / a.P), b = int(i - int64_t(r) * a.P);
+    const int p = parent_state(a.parent, r, b, a.P, a.Bp, a.err);
+    const T* si = static_cast<const T*>(a.state_in) +
+                  (int64_t(r) * a.Bp + p) * (W - 1) * a.C + c;
+    Pack<T, VEC> s[W - 1], x;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) s[j].load(si + int64_t(j) * a.C);
+    x.load(static_cast<const T*>(a.x) + int64_t(r) * a.x_seq + int64_t(b) * a.x_tok + c);
+    float win[W - 1][VEC], xf[VEC], yf[VEC];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) s[j].unpack(win[j]);
+    x.unpack(xf);
+    taps.apply(win, xf, a.silu, yf);
+    Pack<T, VEC> o;
+    o.pack(yf);
+    o.store(static_cast<T*>(a.y) + int64_t(r) * a.y_seq + int64_t(b) * a.y_tok + c);
+    T* so = static_cast<T*>(a.state_out) + i * (W - 1) * a.C + c;
+#pragma unroll
+    for (int j = 0; j < W - 2; ++j) s[j + 1].store(so + int64_t(j) * a.C);
+    x.store(so + int64_t(W - 2) * a.C);
+  }
+}
+
+template <typename T, int VEC, int W>
+cudaError_t run(const ConvArgs& a, bool step, dim3 block, unsigned grid, cudaStream_t st) {
+  if (step)
+    conv_step_kernel<T, VEC, W><<<grid, block, 0, st>>>(a);
+  else
+    conv_kernel<T, VEC, W><<<grid, block, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int VEC>
+cudaError_t by_taps(const ConvArgs& a, int W, bool step, dim3 block, unsigned grid,
+                    cudaStream_t st) {
+  if (W == 2) return run<T, VEC, 2>(a, step, block, grid, st);
+  if (W == 3) return run<T, VEC, 3>(a, step, block, grid, st);
+  return run<T, VEC, 4>(a, step, block, grid, st);
+}
+
+cudaError_t launch(ConvArgs a, int in_dtype, int W, bool wide, bool step, cudaStream_t st) {
+  int sms = 0;
+  cudaError_t e = device_sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const int vec = wide ? (in_dtype == OLA_BF16 ? 8 : 4) : 1;
+  const int64_t nvec = (int64_t(a.C) + vec - 1) / vec;
+  int bx = 8;
+  while (bx < kConvThreads && bx < nvec) bx *= 2;
+  const int by = kConvThreads / bx;
+  a.n_ctile = int((nvec + bx - 1) / bx);
+  // tokens (beams) per thread: as many as leave about 16 blocks of 128 threads for every SM
+  const int64_t rows = step ? int64_t(a.R) * a.P : a.P;
+  const int64_t seqs = step ? 1 : a.R;
+  a.tt = step ? 8 : 32;
+  const int least = step ? 1 : 4;
+  auto blocks = [&](int tt) {
+    const int64_t n = (rows + int64_t(tt) * by - 1) / (int64_t(tt) * by);
+    return (n < 1 ? 1 : n) * seqs * a.n_ctile;
+  };
+  while (a.tt > least && blocks(a.tt) < int64_t(16) * sms) a.tt /= 2;
+  const int64_t grid = blocks(a.tt);
+  a.n_ttile = int(grid / seqs / a.n_ctile);
+  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const dim3 block(bx, by);
+  if (in_dtype == OLA_BF16)
+    return wide ? by_taps<__nv_bfloat16, 8>(a, W, step, block, unsigned(grid), st)
+                : by_taps<__nv_bfloat16, 1>(a, W, step, block, unsigned(grid), st);
+  return wide ? by_taps<float, 4>(a, W, step, block, unsigned(grid), st)
+              : by_taps<float, 1>(a, W, step, block, unsigned(grid), st);
+}
+
+}  // namespace
+
+cudaError_t launch_conv(ConvArgs a, int in_dtype, int W, bool wide, cudaStream_t stream) {
+  return launch(a, in_dtype, W, wide, false, stream);
+}
+
+cudaError_t launch_conv_step(ConvArgs a, int in_dtype, int W, bool wide, cudaStream_t stream) {
+  return launch(a, in_dtype, W, wide, true, stream);
+}
+
+}  // namespace ola
