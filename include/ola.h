@@ -348,7 +348,11 @@ ola_status ola_qk_norm(const ola_qk_desc* d, const void* q, const void* k, const
  *             Calls that may overlap on the GPU need scratch of their own.
  * d_k, d_v in {16, 32, 64, 128, 256}, G divides H, P >= 0. dt * A is taken to be <= 0 (a decay);
  * growth is computed as the formula says as long as it does not overflow. States and sums are
- * fp32, token by token. Long prompts of few sequences are cut into pieces that run side by side and
+ * fp32. bf16 prompts with 16-byte aligned rows and d_k <= 128 run in chunks of 128 tokens on
+ * tensor cores: keys, queries and v enter exactly; the token-to-token weights and the copy of
+ * the state that meets the queries are rounded to bf16 on the way to y (y itself is bf16), the
+ * products that build the state are not (S_out is good to fp32). Everything else runs token by
+ * token in fp32. Long prompts of few sequences are cut into pieces that run side by side and
  * are joined through `ws`. Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 typedef struct {
   int32_t R, P, H, G, d_k, d_v;

@@ -346,6 +346,11 @@ ola_status ola_scan_workspace_bytes(const ola_scan_desc* d, uint64_t* out_bytes)
   int n = 1, len = 0;
   const int sms = sm_count();
   scan_tok_pieces(d->R, d->P, d->H, d->d_k, d->d_v, sms, &n, &len);
+  if (d->in_dtype == OLA_BF16) {
+    int n2 = 1;
+    scan_chunk_pieces(d->R, d->P, d->H, d->d_v, sms, &n2, &len);
+    n = n2 > n ? n2 : n;
+  }
   *out_bytes = ws_bytes_for(d, n);
   return OLA_OK;
 }
@@ -365,7 +370,11 @@ ola_status ola_scan(const ola_scan_desc* d, const void* v, const float* dt, cons
   for (const Rows* x : {&t.v, &t.k, &t.q, &t.z, &t.y})
     if (overlap(*x, so)) return OLA_ERR_INVALID_ARG;
   if (overlap(t.y, si)) return OLA_ERR_INVALID_ARG;
-  scan_tok_pieces(d->R, d->P, d->H, d->d_k, d->d_v, sm_count(), &a.nseg, &a.seg_len);
+  const bool chunked = scan_chunk_supported(a, d->in_dtype);
+  if (chunked)
+    scan_chunk_pieces(d->R, d->P, d->H, d->d_v, sm_count(), &a.nseg, &a.seg_len);
+  else
+    scan_tok_pieces(d->R, d->P, d->H, d->d_k, d->d_v, sm_count(), &a.nseg, &a.seg_len);
   const uint64_t need = ws_bytes_for(d, a.nseg);
   if (need) {
     if (!ws || ws_bytes < need || !aligned(ws, 16)) return OLA_ERR_INVALID_ARG;
@@ -380,7 +389,8 @@ ola_status ola_scan(const ola_scan_desc* d, const void* v, const float* dt, cons
   a.S_in = S_in;
   a.lens = lens;
   a.S_out = S_out;
-  return from_cuda(launch_scan_tok(a, d->in_dtype, static_cast<cudaStream_t>(stream)));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return from_cuda(chunked ? launch_scan_chunk(a, st) : launch_scan_tok(a, d->in_dtype, st));
 }
 
 ola_status ola_scan_step(const ola_scan_desc* d, int32_t Bp, const void* v, const float* dt,

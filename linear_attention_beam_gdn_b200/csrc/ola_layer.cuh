@@ -158,4 +158,8 @@ cudaError_t launch_scan_join(const ScanArgs& a, cudaStream_t stream);
 cudaError_t launch_scan_step(const ScanArgs& a, int in_dtype, cudaStream_t stream);
 void scan_tok_pieces(int R, int P, int H, int d_k, int d_v, int sms, int* nseg, int* seg_len);
 
+bool scan_chunk_supported(const ScanArgs& a, int in_dtype);
+void scan_chunk_pieces(int R, int P, int H, int d_v, int sms, int* nseg, int* seg_len);
+cudaError_t launch_scan_chunk(const ScanArgs& a, cudaStream_t stream);
+
 }  // namespace ola

@@ -1,0 +1,760 @@
+// Selective state space scan of bf16 prompts in chunks of 128 tokens on tensor cores, d_k <= 128.
+//
+//     S <- exp(dt A) S + dt v k^T,   o = S q + D v,   y = o * SiLU(z)
+//
+// Over a chunk entered with state S0, with c_t = sum_{i<=t} dt_i A (a log decay, <= 0):
+//     o_t = e^{c_t} S0 q_t + sum_{s<=t} e^{c_t - c_s} dt_s (q_t . k_s) v_s
+//     S_C = e^{c_C} S0 + sum_s (e^{c_C - c_s} dt_s v_s) k_s^T
+// as four products per chunk, each with fp32 accumulation in tensor memory:
+//     G  = Q K^T              128 x 128 x d_k     (exact bf16 operands)
+//     Y1 = P V                128 x 64 x 128      P = G * decay * dt below the diagonal, as bf16
+//     Y2 = Q S0^T             128 x 64 x d_k      S0 as bf16; o = Y1 + e^{c_t} Y2
+//     dS = K^T (W V)          d_k x 64 x 128      W V in three bf16 parts (24 bits)
+// The state itself stays in fp32 registers and never meets a rounded operand: S_C is as exact as
+// an fp32 sum. P and the copy of S0 are rounded to bf16 on the way to y alone, which is bf16.
+//
+// No exponent is ever positive: inside a block of 32 tokens P takes exp2 of the difference of two
+// running sums, between blocks s < t it is (e^{c_t - end of s's block}) (e^{end - c_s} dt_s), a
+// factor per row and one per column.
+//
+// One block per (sequence, head, 64 value columns, piece), one per SM:
+//   warps 0-3    G -> P (thread = token t; P into tensor memory as the A operand of Y1)
+//   warps 4-7    the chunk's scalars (dt, running sums) and W V (thread = token s)
+//   warps 8-11   state rows (thread = key column, 64 fp32 of S^T): S = e^{c_C} S + dS, its bf16 copy
+//   warps 12-15  outputs (thread = token t): Y1 + e^{c_t} Y2, D, gate; y staged over v, stored by TMA
+//   warp 16      TMA: v, k, q tiles;   warp 17  tcgen05.mma
+// Nothing but Y2 waits for the state, so the products of a chunk overlap the conversions of its
+// neighbours. A piece of a cut sequence runs twice: dS alone first (FULL = false), then, once
+// scan_join_kernel has made the state before every piece, the outputs.
+#include "ola_layer.cuh"
+
+namespace ola {
+
+namespace {
+
+constexpr int kQ = 128;                 // tokens per chunk
+constexpr int kNV = 64;                 // value columns per block
+constexpr int kThr = 576;
+constexpr uint32_t kBlk = kQ * 128;     // 16 KB: 128 rows of 64 bf16 columns
+
+// tensor memory columns
+constexpr uint32_t kTG = 0;             // G, 128
+constexpr uint32_t kTP = 128;           // P as bf16 pairs, 64
+constexpr uint32_t kTD = 192;           // dS of the three parts of W V, 64 each
+constexpr uint32_t kTY1 = 384;
+constexpr uint32_t kTY2 = 448;
+
+constexpr int kScFloats = 356;          // loc[128], dt[128], colf[96], block sums[4]
+
+template <int KB>                       // 64-column blocks of d_k
+struct Lay {
+  static constexpr int NST = KB == 2 ? 2 : 3;              // stages
+  static constexpr uint32_t kK = 0;                        // keys, then queries, then values
+  static constexpr uint32_t kQr = KB * kBlk;
+  static constexpr uint32_t kV = 2 * KB * kBlk;
+  static constexpr uint32_t kStage = (2 * KB + 1) * kBlk;
+  static constexpr uint32_t kXw = NST * kStage;            // W V: three parts
+  static constexpr uint32_t kS = kXw + 3 * kBlk;           // state copy [64 KB rows][64 columns]
+  static constexpr uint32_t kSc = kS + KB * 8192;          // scalars per stage
+  static constexpr uint32_t kBar = kSc + NST * kScFloats * 4;
+  static constexpr int kNBar = 3 * NST + 11;
+  static constexpr uint32_t kBytes = kBar + kNBar * 8 + 16;
+};
+static_assert(Lay<1>::kBar % 8 == 0 && Lay<2>::kBar % 8 == 0, "mbarriers");
+static_assert(Lay<1>::kBytes <= 232448 && Lay<2>::kBytes <= 232448, "shared memory per block");
+static_assert((kScFloats * 4) % 16 == 0, "float4 rows of scalars");
+
+struct ChunkScan {
+  CUtensorMap mv, mk, mq, my;           // [R][P][heads][d] bf16, boxes of 64 x 1 x 128 x 1
+  ScanArgs a;
+  int ntile;                            // blocks of 64 value columns
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// 32 consecutive columns of this thread's tensor-memory lane; the wait comes with tmem_ld_wait.
+__device__ __forceinline__ void tmem_ld32_raw(uint32_t t, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t)
+      : "memory");
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int c0,
+                                             int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::
+          "l"(reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase) {
+  return __all_sync(kFull, mbar_wait_bounded(bar, uint32_t(phase) & 1u));
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// Barrier over `count` threads that returns the AND of `v` over them: a group of warps whose waits
+// may run out leaves its loop together.
+__device__ __forceinline__ bool bar_and(int id, int count, bool v) {
+  uint32_t out;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(out)
+      : "r"(uint32_t(v)), "r"(id), "r"(count)
+      : "memory");
+  return out != 0;
+}
+
+template <int KB, bool FULL>
+__global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_constant__ ChunkScan c) {
+  using Y = Lay<KB>;
+  constexpr int NST = Y::NST;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Y::kBar);
+  uint64_t* full = bar;                  // [NST] tiles landed (TMA bytes)
+  uint64_t* empty = bar + NST;           // [NST] stage and scalars reusable
+  uint64_t* sc_full = bar + 2 * NST;     // [NST] scalars written (4 warps)
+  uint64_t* one = bar + 3 * NST;
+  uint64_t* xw_full = one + 0;           // W V written (4 warps)
+  uint64_t* ds_full = one + 1;           // dS done (and W V read)
+  uint64_t* ds_free = one + 2;           // dS read (4 warps)
+  uint64_t* g_full = one + 3;            // G done
+  uint64_t* g_free = one + 4;            // G read (4 warps)
+  uint64_t* p_full = one + 5;            // P written (4 warps)
+  uint64_t* s_full = one + 6;            // state copy written (4 warps)
+  uint64_t* s_free = one + 7;            // Y2 done: state copy read
+  uint64_t* y_full = one + 8;            // Y1 and Y2 done (and P read)
+  uint64_t* y_free = one + 9;            // Y1 and Y2 read (4 warps)
+  uint64_t* done = one + 10;             // every MMA completed
+  uint32_t* holder = reinterpret_cast<uint32_t*>(bar + Y::kNBar);
+  const ScanArgs& a = c.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // block -> (sequence, head, value columns, piece); neighbours share keys and queries
+  const int nseg = FULL ? a.nseg : a.nseg - 1;
+  const int tile = blockIdx.x % c.ntile;
+  const int rest = blockIdx.x / c.ntile;
+  const int rh = rest % (a.R * a.H), seg = rest / (a.R * a.H);
+  const int r = rh / a.H, h = rh - r * a.H, g = h / (a.H / a.G);
+  const int L = seq_len(a.lens, r, a.P);
+  const int64_t pb = int64_t(seg) * a.seg_len;
+  const int p0 = int(pb < L ? pb : L), p1 = int(pb + a.seg_len < L ? pb + a.seg_len : L);
+  const int nch = (p1 - p0 + kQ - 1) / kQ;
+
+  if (smem_u32(sm) & 1023u) {              // the swizzled tiles' alignment; the whole block leaves
+    if (tid == 0) report_error(a.err, OLA_ERR_CUDA, 59, 0);
+    return;
+  }
+  if (tid == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&full[s], 1);
+      // MMA commit, state warps, and the block of output warps
+      mbar_init(&empty[s], FULL ? 6 : 5);
+      mbar_init(&sc_full[s], 4);
+    }
+    mbar_init(xw_full, 4);
+    mbar_init(ds_full, 1);
+    mbar_init(ds_free, 4);
+    mbar_init(g_full, 1);
+    mbar_init(g_free, 4);
+    mbar_init(p_full, 4);
+    mbar_init(s_full, 4);
+    mbar_init(s_free, 1);
+    mbar_init(y_full, 1);
+    mbar_init(y_free, 4);
+    mbar_init(done, 1);
+    fence_barrier_init();
+  }
+  if (warp == 17) tmem_alloc(holder, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  const uint32_t base = smem_u32(sm);
+
+  if (warp == 16) {
+    // ------------------------------------------------------------------ TMA loads
+    if (lane == 0) {
+      prefetch_tmap(&c.mk);
+      prefetch_tmap(&c.mv);
+      if (FULL) prefetch_tmap(&c.mq);
+      constexpr uint32_t bytes = (FULL ? 2 * KB + 1 : KB + 1) * kBlk;
+      int issued = 0;
+      for (int i = 0; i < nch; ++i) {
+        const int s = i % NST, n = i / NST;
+        if (n > 0 && !mbar_wait_bounded(&empty[s], (n - 1) & 1)) {
+          report_error(a.err, OLA_ERR_TIMEOUT, 60, i);
+          break;
+        }
+        mbar_arrive_expect_tx(&full[s], bytes);
+        unsigned char* st = sm + s * Y::kStage;
+        const int p = p0 + i * kQ;
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+          tma_load_4d(st + Y::kK + b * kBlk, &c.mk, &full[s], 64 * b, g, p, r);
+          if (FULL) tma_load_4d(st + Y::kQr + b * kBlk, &c.mq, &full[s], 64 * b, g, p, r);
+        }
+        tma_load_4d(st + Y::kV, &c.mv, &full[s], kNV * tile, h, p, r);
+        issued = i + 1;
+      }
+      // the copies still in flight land before the block exits
+      for (int i = issued > NST ? issued - NST : 0; i < issued; ++i)
+        mbar_wait_bounded(&full[i % NST], (i / NST) & 1);
+    }
+  } else if (warp == 17) {
+    // ------------------------------------------------------------------ products
+    const uint32_t id_g = idesc_bf16_f32(128, 128);
+    const uint32_t id_y = idesc_bf16_f32(128, kNV) | (1u << 16);               // B MN-major
+    const uint32_t id_d = idesc_bf16_f32_amn(128, 3 * kNV) | (1u << 16);       // A, B MN-major
+    auto issue_g = [&](int i) -> bool {
+      const int s = i % NST;
+      if (!warp_wait(&full[s], i / NST) || (i > 0 && !warp_wait(g_free, i - 1))) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t dq = sw128_kmajor_desc(base + s * Y::kStage + Y::kQr);
+        const uint64_t dk = sw128_kmajor_desc(base + s * Y::kStage + Y::kK);
+#pragma unroll
+        for (int k = 0; k < 4 * KB; ++k) {
+          const uint64_t off = (k >> 2) * (kBlk >> 4) + (k & 3) * 2;
+          umma_bf16(tmem + kTG, dq + off, dk + off, id_g, k != 0);
+        }
+        umma_commit(g_full);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = !FULL || nch == 0 || issue_g(0);
+    for (int i = 0; i < nch && ok; ++i) {
+      const int s = i % NST;
+      const uint32_t st = base + s * Y::kStage;
+      // dS: A = keys read MN-major (key columns along M; for d_k <= 64 the upper 64 rows read the
+      // next tile and are not used), B = the three parts of W V side by side
+      ok = warp_wait(&full[s], i / NST) && warp_wait(xw_full, i) &&
+           (i == 0 || warp_wait(ds_free, i - 1));
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t dk = sw128_mnmajor_desc(st + Y::kK, kBlk, 1024);
+        const uint64_t dx = sw128_mnmajor_desc(base + Y::kXw, kBlk, 1024);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          umma_bf16(tmem + kTD, dk + k * 128, dx + k * 128, id_d, k != 0);
+        umma_commit(ds_full);
+        if (!FULL) umma_commit(&empty[s]);
+      }
+      __syncwarp();
+      if (!FULL) continue;
+      // Y2: A = queries, B = the state copy (rows = key columns)
+      ok = warp_wait(s_full, i) && (i == 0 || warp_wait(y_free, i - 1));
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t dq = sw128_kmajor_desc(st + Y::kQr);
+        const uint64_t dsd = sw128_mnmajor_desc(base + Y::kS, kBlk, 1024);
+#pragma unroll
+        for (int k = 0; k < 4 * KB; ++k)
+          umma_bf16(tmem + kTY2, dq + (k >> 2) * (kBlk >> 4) + (k & 3) * 2, dsd + k * 128, id_y,
+                    k != 0);
+        umma_commit(s_free);
+      }
+      __syncwarp();
+      if (i + 1 < nch && !(ok = issue_g(i + 1))) break;
+      // Y1: A = P in tensor memory, B = the values (rows = tokens)
+      ok = warp_wait(p_full, i);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t dv = sw128_mnmajor_desc(st + Y::kV, kBlk, 1024);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          umma_bf16_ts(tmem + kTY1, tmem + kTP + k * 8, dv + k * 128, id_y, k != 0);
+        umma_commit(y_full);
+        umma_commit(&empty[s]);
+      }
+      __syncwarp();
+    }
+    if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 61, 0);
+    if (elect_one()) umma_commit(done);
+    __syncwarp();
+    mbar_wait_bounded(done, 0);              // before tensor memory is released
+    __syncwarp();
+  } else if (warp < 4) {
+    // ------------------------------------------------------------------ G -> P
+    if (FULL) {
+      const int t = 32 * warp + lane;
+      const uint32_t tl = tmem + (uint32_t(32 * warp) << 16);
+      {
+        const uint4 z[4] = {};
+#pragma unroll 1
+        for (int j = warp + 1; j < 4; ++j) tmem_st16(tl + kTP + 16 * j, z);   // above the diagonal
+        tmem_st_wait();
+      }
+      bool ok = true;
+      for (int i = 0; i < nch; ++i) {
+        const int s = i % NST;
+        ok = warp_wait(&sc_full[s], i / NST) && warp_wait(g_full, i) &&
+             (i == 0 || warp_wait(y_full, i - 1));
+        if (!ok) break;
+        tc_fence_after();
+        const float* loc = reinterpret_cast<const float*>(sm + Y::kSc) + s * kScFloats;
+        const float* dts = loc + 128;
+        const float* colf = loc + 256;
+        const float* bs = loc + 352;
+        const float mine = loc[t];
+        float mid = mine;                    // log2 decay from the end of block j to t
+#pragma unroll 1
+        for (int j = warp; j >= 0; --j) {
+          uint32_t x[32];
+          tmem_ld32_raw(tl + kTG + 32 * j, x);
+          uint32_t p[16];
+          if (j == warp) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float4 l4 = *reinterpret_cast<const float4*>(loc + 32 * j + 4 * q);
+              const float4 d4 = *reinterpret_cast<const float4*>(dts + 32 * j + 4 * q);
+              const float lv[4] = {l4.x, l4.y, l4.z, l4.w}, dv[4] = {d4.x, d4.y, d4.z, d4.w};
+              float f[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                f[e] = 4 * q + e <= lane
+                           ? __uint_as_float(x[4 * q + e]) * (ex2(mine - lv[e]) * dv[e])
+                           : 0.f;
+              p[2 * q] = pack2(f[0], f[1]);
+              p[2 * q + 1] = pack2(f[2], f[3]);
+            }
+          } else {
+            const float rf = ex2(mid);
+            mid += bs[j];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float4 c4 = *reinterpret_cast<const float4*>(colf + 32 * j + 4 * q);
+              p[2 * q] = pack2(__uint_as_float(x[4 * q]) * (rf * c4.x),
+                               __uint_as_float(x[4 * q + 1]) * (rf * c4.y));
+              p[2 * q + 1] = pack2(__uint_as_float(x[4 * q + 2]) * (rf * c4.z),
+                                   __uint_as_float(x[4 * q + 3]) * (rf * c4.w));
+            }
+          }
+          uint4 v4[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            v4[q] = make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
+          tmem_st16(tl + kTP + 16 * j, v4);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(g_free);
+          mbar_arrive(p_full);
+        }
+      }
+      if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 62, 0);
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------ scalars and W V
+    const int t = tid - 128, w4 = warp - 4;
+    const float A2 = a.A[h] * 1.4426950408889634f;
+    const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+    const float* dtp = a.dt + int64_t(r) * a.P * a.H + h;
+    auto load_dt = [&](int i) -> float {
+      const int p = p0 + i * kQ + t;
+      return i < nch && p < p1 ? __ldg(dtp + int64_t(p) * a.H) : 0.f;
+    };
+    float raw = load_dt(0);
+    bool ok = true;
+    for (int i = 0; i < nch; ++i) {
+      const int s = i % NST, n = i / NST;
+      const int left = p1 - (p0 + i * kQ);              // tokens of the piece from here on
+      // tokens behind the end take no part: dt = 0
+      float dt = raw + bias;
+      if (a.softplus) dt = softplus_f(dt);
+      if (t >= left) dt = 0.f;
+      raw = load_dt(i + 1);
+      // a decay below 2^-256 is 0; the clamp keeps sums of resets finite
+      const float g2 = fmaxf(dt * A2, -256.f);
+      float pre = g2, suf = g2;                          // inclusive sums over the warp's 32 tokens
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float u = __shfl_up_sync(kFull, pre, o), d = __shfl_down_sync(kFull, suf, o);
+        if (lane >= o) pre += u;
+        if (lane + o < 32) suf += d;
+      }
+      float after = __shfl_down_sync(kFull, suf, 1);     // tokens of the block behind t
+      if (lane == 31) after = 0.f;
+      ok = ok && (n == 0 || warp_wait(&empty[s], n - 1));
+      float* loc = reinterpret_cast<float*>(sm + Y::kSc) + s * kScFloats;
+      if (ok) {
+        loc[t] = pre;
+        loc[128 + t] = dt;
+        if (w4 < 3) loc[256 + t] = dt * ex2(after);
+        if (lane == 31) loc[352 + w4] = pre;
+      }
+      if (!(ok = bar_and(1, 128, ok))) break;
+      if (lane == 0) mbar_arrive(&sc_full[s]);
+      for (int j = w4 + 1; j < 4; ++j) after += loc[352 + j];
+      const float w = dt * exp2f(after);
+      // (a wait that ran out is acted on at the next barrier of the four warps)
+      ok = warp_wait(&full[s], n) && (i == 0 || warp_wait(ds_full, i - 1));
+      if (!ok) continue;
+      unsigned char* vrow = sm + s * Y::kStage + Y::kV + t * 128;
+      unsigned char* xrow = sm + Y::kXw + t * 128;
+      if (t >= left) {
+        // padding may hold anything, also NaN: its key and value rows are cleared
+        const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          reinterpret_cast<uint4*>(vrow)[q] = z;
+#pragma unroll
+          for (int b = 0; b < KB; ++b)
+            reinterpret_cast<uint4*>(sm + s * Y::kStage + Y::kK + b * kBlk + t * 128)[q] = z;
+        }
+      }
+#pragma unroll 2
+      for (int q = 0; q < 8; ++q) {
+        const uint32_t off = uint32_t((q ^ (t & 7)) << 4);
+        const uint4 v4 = *reinterpret_cast<const uint4*>(vrow + off);
+        const uint32_t vw[4] = {v4.x, v4.y, v4.z, v4.w};
+        uint32_t h1[4], h2[4], h3[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float f0 = lo_f(vw[e]) * w, f1 = hi_f(vw[e]) * w;
+          h1[e] = pack2(f0, f1);
+          f0 -= lo_f(h1[e]);
+          f1 -= hi_f(h1[e]);
+          h2[e] = pack2(f0, f1);
+          f0 -= lo_f(h2[e]);
+          f1 -= hi_f(h2[e]);
+          h3[e] = pack2(f0, f1);
+        }
+        *reinterpret_cast<uint4*>(xrow + off) = make_uint4(h1[0], h1[1], h1[2], h1[3]);
+        *reinterpret_cast<uint4*>(xrow + kBlk + off) = make_uint4(h2[0], h2[1], h2[2], h2[3]);
+        *reinterpret_cast<uint4*>(xrow + 2 * kBlk + off) = make_uint4(h3[0], h3[1], h3[2], h3[3]);
+      }
+      fence_proxy_async_smem();
+      warp_arrive(xw_full);
+    }
+    if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 63, 0);
+  } else if (warp < 12) {
+    // ------------------------------------------------------------------ state rows
+    const int k = tid - 256, w4 = warp - 8;
+    const uint32_t tl = tmem + (uint32_t(32 * w4) << 16);
+    const bool mine = k < a.d_k, holds = k < 64 * KB;    // a key column, a row of the copy
+    const float* entering = nullptr;
+    if (FULL)
+      entering = a.nseg > 1 ? a.seg_S + (int64_t(rh) * a.nseg + seg) * a.d_v * a.d_k
+                            : (a.S_in ? a.S_in + int64_t(rh) * a.d_v * a.d_k : nullptr);
+    const int v0 = kNV * tile, nv = min(kNV, a.d_v - v0);
+    float S[kNV];
+#pragma unroll
+    for (int v = 0; v < kNV; ++v)
+      S[v] = entering && mine && v < nv ? entering[int64_t(v0 + v) * a.d_k + k] : 0.f;
+    // the bf16 copy: row k of 64 value columns, 128-byte swizzle
+    auto copy_out = [&]() {
+      if (holds) {
+        unsigned char* row = sm + Y::kS + k * 128;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          *reinterpret_cast<uint4*>(row + ((q ^ (k & 7)) << 4)) =
+              make_uint4(pack2(S[8 * q], S[8 * q + 1]), pack2(S[8 * q + 2], S[8 * q + 3]),
+                         pack2(S[8 * q + 4], S[8 * q + 5]), pack2(S[8 * q + 6], S[8 * q + 7]));
+      }
+      fence_proxy_async_smem();
+      warp_arrive(s_full);
+    };
+    if (FULL && nch > 0) copy_out();
+    double logsum = 0.0;
+    bool ok = true;
+    for (int i = 0; i < nch; ++i) {
+      const int s = i % NST;
+      ok = warp_wait(&sc_full[s], i / NST) && warp_wait(ds_full, i);
+      if (!ok) break;
+      tc_fence_after();
+      const float4 b4 = *reinterpret_cast<const float4*>(
+          reinterpret_cast<const float*>(sm + Y::kSc) + s * kScFloats + 352);
+      const float total = (b4.x + b4.y) + (b4.z + b4.w);
+      warp_arrive(&empty[s]);
+      if (!FULL) logsum += double(total);
+      // e^{c_C} S as S + (e^{c_C} - 1) S where the decay is slow, so that it is not rounded chunk
+      // after chunk; a fast decay would cancel in that form and is taken as it is
+      const float x = total * 0.69314718055994531f;
+      const bool slow = x > -0.5f;
+      const float mul = slow ? expm1f(x) : expf(x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        float x0[8], x1[8], x2[8], x3[8];
+        // (the fourth load repeats the third: one wait for all)
+        tmem_ld8x4(tl + kTD + 8 * q, tl + kTD + 64 + 8 * q, tl + kTD + 128 + 8 * q,
+                   tl + kTD + 128 + 8 * q, x0, x1, x2, x3);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float own = x0[e] + (x1[e] + x2[e]), old = S[8 * q + e];
+          S[8 * q + e] = fmaf(mul, old, slow ? old + own : own);
+        }
+      }
+      tc_fence_before();
+      warp_arrive(ds_free);
+      if (FULL && i + 1 < nch) {
+        if (!(ok = warp_wait(s_free, i))) break;
+        copy_out();
+      }
+    }
+    if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 64, 0);
+    float* out = nullptr;
+    if (!FULL)
+      out = a.seg_S + (int64_t(rh) * a.nseg + seg) * a.d_v * a.d_k;
+    else if (seg == nseg - 1 && a.S_out)
+      out = a.S_out + int64_t(rh) * a.d_v * a.d_k;
+    if (out && mine) {
+#pragma unroll
+      for (int v = 0; v < kNV; ++v)
+        if (v < nv) out[int64_t(v0 + v) * a.d_k + k] = S[v];
+    }
+    if (!FULL && tile == 0 && k == 0)
+      a.seg_a[int64_t(rh) * a.nseg + seg] = float(exp2(logsum));
+  } else {
+    // ------------------------------------------------------------------ outputs
+    if (FULL) {
+      const int t = tid - 384, w4 = warp - 12;
+      const uint32_t tl = tmem + (uint32_t(32 * w4) << 16);
+      const int v0 = kNV * tile, nv = min(kNV, a.d_v - v0);
+      const float D = a.D ? a.D[h] : 0.f;
+      const __nv_bfloat16* zp =
+          a.z ? static_cast<const __nv_bfloat16*>(a.z) + int64_t(r) * a.z_seq + int64_t(h) * a.d_v +
+                    v0
+              : nullptr;
+      __nv_bfloat16* yp = static_cast<__nv_bfloat16*>(a.y) + int64_t(r) * a.y_seq +
+                          int64_t(h) * a.d_v + v0;
+      bool ok = true;
+      for (int i = 0; i < nch; ++i) {
+        const int s = i % NST;
+        const int p = p0 + i * kQ + t;
+        const bool live = p < p1;
+        uint4 zr[8];
+        if (a.z) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            zr[q] = make_uint4(0, 0, 0, 0);
+            if (live && 8 * q < nv)
+              zr[q] = __ldg(reinterpret_cast<const uint4*>(zp + int64_t(p) * a.z_tok) + q);
+          }
+        }
+        ok = warp_wait(&sc_full[s], i / NST) && warp_wait(y_full, i);
+        if (!bar_and(2, 128, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float* loc = reinterpret_cast<const float*>(sm + Y::kSc) + s * kScFloats;
+        float cum = loc[t];
+        for (int j = 0; j < w4; ++j) cum += loc[352 + j];
+        const float ec = ex2(cum);
+        unsigned char* vrow = sm + s * Y::kStage + Y::kV + t * 128;
+        // whole rows go out by TMA (rows past P are clipped); a sequence that ends inside the
+        // chunk but before P is stored row by row
+        const bool by_tma = p0 + (i + 1) * kQ <= p1 || p1 == a.P;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t x1[32], x2[32];
+          tmem_ld32_raw(tl + kTY1 + 32 * half, x1);
+          tmem_ld32_raw(tl + kTY2 + 32 * half, x2);
+          if (half == 1) {
+            tc_fence_before();
+            warp_arrive(y_free);
+          }
+#pragma unroll
+          for (int qq = 0; qq < 4; ++qq) {
+            const int q = 4 * half + qq;
+            unsigned char* at = vrow + ((q ^ (t & 7)) << 4);
+            const uint4 v4 = *reinterpret_cast<const uint4*>(at);
+            const uint32_t vw[4] = {v4.x, v4.y, v4.z, v4.w};
+            const uint32_t zw[4] = {zr[q].x, zr[q].y, zr[q].z, zr[q].w};
+            uint32_t ow[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int at0 = 8 * qq + 2 * e;
+              float o0 = fmaf(ec, __uint_as_float(x2[at0]), __uint_as_float(x1[at0]));
+              float o1 = fmaf(ec, __uint_as_float(x2[at0 + 1]), __uint_as_float(x1[at0 + 1]));
+              if (a.D) {
+                o0 = fmaf(D, lo_f(vw[e]), o0);
+                o1 = fmaf(D, hi_f(vw[e]), o1);
+              }
+              if (a.z) {
+                o0 *= silu_f<__nv_bfloat16>(lo_f(zw[e]));
+                o1 *= silu_f<__nv_bfloat16>(hi_f(zw[e]));
+              }
+              ow[e] = pack2(o0, o1);
+            }
+            const uint4 o4 = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+            if (by_tma)
+              *reinterpret_cast<uint4*>(at) = o4;
+            else if (live && 8 * q < nv)
+              *(reinterpret_cast<uint4*>(yp + int64_t(p) * a.y_tok) + q) = o4;
+          }
+        }
+        if (by_tma) fence_proxy_async_smem();
+        named_bar_sync(2, 128);               // nothing between the two barriers can run out
+        if (t == 0) {
+          if (by_tma) {
+            tma_store_4d(&c.my, sm + s * Y::kStage + Y::kV, v0, h, p0 + i * kQ, r);
+            bulk_commit();
+            bulk_wait_read();
+          }
+          mbar_arrive(&empty[s]);
+        }
+      }
+      if (t == 0) bulk_wait_all();
+      if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 65, 0);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 17) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------- host side
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                             const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn map_encoder() {
+  static std::atomic<EncodeFn> fn{nullptr};
+  EncodeFn f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess) {
+      f = reinterpret_cast<EncodeFn>(p);
+      fn.store(f, std::memory_order_release);
+    }
+  }
+  return f;
+}
+
+// [R][P][heads][d] bf16 with the given strides as a 4-D map (column, head, token, sequence) of
+// 64 x 1 x 128 x 1 boxes, 128-byte swizzle. Columns past d and tokens past P read 0 and are not
+// written.
+bool rows_map(CUtensorMap* map, const void* base, int d, int heads, int P, int R, int64_t tok,
+              int64_t seq) {
+  EncodeFn fn = map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(P), cuuint64_t(R)};
+  cuuint64_t strides[3] = {cuuint64_t(d) * 2, cuuint64_t(tok) * 2, cuuint64_t(seq) * 2};
+  cuuint32_t box[4] = {64, 1, kQ, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+            es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int KB>
+cudaError_t run(const ChunkScan& c, cudaStream_t st) {
+  constexpr uint32_t bytes = Lay<KB>::kBytes;
+  static std::atomic<uint64_t> set{0};
+  cudaError_t e = once_per_device(set, [&] {
+    cudaError_t x = cudaFuncSetAttribute(scan_chunk_kernel<KB, true>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return x != cudaSuccess
+               ? x
+               : cudaFuncSetAttribute(scan_chunk_kernel<KB, false>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
+  if (e != cudaSuccess) return e;
+  const int64_t chains = int64_t(c.a.R) * c.a.H * c.ntile;
+  if (c.a.nseg > 1) {
+    scan_chunk_kernel<KB, false><<<unsigned(chains * (c.a.nseg - 1)), kThr, bytes, st>>>(c);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_scan_join(c.a, st)) != cudaSuccess) return e;
+  }
+  scan_chunk_kernel<KB, true><<<unsigned(chains * c.a.nseg), kThr, bytes, st>>>(c);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool scan_chunk_supported(const ScanArgs& a, int in_dtype) {
+  if (in_dtype != OLA_BF16 || a.d_k > 128 || a.P < 1) return false;
+  // 16-byte rows, strides within the tensor map's 2^40 bytes
+  auto ok = [&](const void* p, int64_t tok, int64_t seq) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && tok % 8 == 0 && seq % 8 == 0 &&
+           tok < (int64_t(1) << 39) && seq < (int64_t(1) << 39);
+  };
+  return ok(a.v, a.v_tok, a.v_seq) && ok(a.k, a.k_tok, a.k_seq) && ok(a.q, a.q_tok, a.q_seq) &&
+         ok(a.y, a.y_tok, a.y_seq) && (!a.z || ok(a.z, a.z_tok, a.z_seq));
+}
+
+// Pieces: one block runs per SM, so a batch that leaves at least half of them idle is cut into as
+// many pieces as fill them.
+void scan_chunk_pieces(int R, int P, int H, int d_v, int sms, int* nseg, int* seg_len) {
+  const int64_t chains = int64_t(R) * H * ((d_v + kNV - 1) / kNV);
+  const int64_t chunks = (int64_t(P) + kQ - 1) / kQ;
+  int64_t want = sms / chains;
+  if (want > chunks) want = chunks;
+  if (want < 2) want = 1;
+  const int64_t per = want > 0 ? (chunks + want - 1) / want : 1;
+  *seg_len = int((per < 1 ? 1 : per) * kQ);
+  *nseg = int((int64_t(P) + *seg_len - 1) / *seg_len);
+  if (*nseg < 1) *nseg = 1;
+}
+
+cudaError_t launch_scan_chunk(const ScanArgs& a, cudaStream_t st) {
+  ChunkScan c;
+  c.a = a;
+  c.ntile = (a.d_v + kNV - 1) / kNV;
+  if (!rows_map(&c.mv, a.v, a.d_v, a.H, a.P, a.R, a.v_tok, a.v_seq) ||
+      !rows_map(&c.mk, a.k, a.d_k, a.G, a.P, a.R, a.k_tok, a.k_seq) ||
+      !rows_map(&c.mq, a.q, a.d_k, a.G, a.P, a.R, a.q_tok, a.q_seq) ||
+      !rows_map(&c.my, a.y, a.d_v, a.H, a.P, a.R, a.y_tok, a.y_seq))
+    return cudaErrorInvalidValue;
+  return a.d_k <= 64 ? run<1>(c, st) : run<2>(c, st);
+}
+
+}  // namespace ola

@@ -127,5 +127,14 @@ def scan(v, dt, A, k, q, D, dt_bias, z, S_in, lens, use_softplus, out0, chunked=
                     if t == torch.bfloat16 else eo * gate.abs() + 12 * U * (o * gate).abs()
             y[r, p] = o
             toly[r, p] = eo + HALF[t] * o.abs()
+        if chunked:
+            # A chunk's own contributions are summed by 8 accumulation steps of 16 products. A step
+            # aligns its addends to the largest and cuts them at 24 bits or more: up to 2 U of it
+            # for the accumulator and for each of the 16 products, so 8 * 2 U + 16 * 2 U of the
+            # sum of |contributions| at most (the second and third bf16 part of a weight add
+            # 2^-8 of that). These errors decay with the contributions, so over all chunks they
+            # stay below 50 U of M. (The weights' exponents are covered above: a sum of at most 8
+            # additions of terms off by 3 U is off by 11 U of itself, below step_rel's 16 U.)
+            E = E + 50 * U * M
         S[r], tolS[r] = T, E
     return y, S, toly + 1e-30, tolS + 1e-30
