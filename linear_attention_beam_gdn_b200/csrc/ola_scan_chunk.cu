@@ -19,10 +19,11 @@
 //
 // One block per (sequence, head, 64 value columns, piece), one per SM:
 //   warps 0-3    G -> P (thread = token t; P into tensor memory as the A operand of Y1)
-//   warps 4-7    the chunk's scalars (dt, running sums) and W V (thread = token s)
+//   warps 4-7    W V (thread = token s)
 //   warps 8-11   state rows (thread = key column, 64 fp32 of S^T): S = e^{c_C} S + dS, its bf16 copy
-//   warps 12-15  outputs (thread = token t): Y1 + e^{c_t} Y2, D, gate; y staged over v, stored by TMA
-//   warp 16      TMA: v, k, q tiles;   warp 17  tcgen05.mma
+//   warps 12-15  outputs (thread = token t): Y1 + e^{c_t} Y2, D, gate; y staged over v
+//   warp 16      TMA loads of keys and queries;   warp 17  tcgen05.mma
+//   warp 18      TMA stores of y and loads of v;  warp 19  the chunk's scalars (dt, running sums)
 // Nothing but Y2 waits for the state, so the products of a chunk overlap the conversions of its
 // neighbours. A piece of a cut sequence runs twice: dS alone first (FULL = false), then, once
 // scan_join_kernel has made the state before every piece, the outputs.
@@ -34,30 +35,30 @@ namespace {
 
 constexpr int kQ = 128;                 // tokens per chunk
 constexpr int kNV = 64;                 // value columns per block
-constexpr int kThr = 576;
+constexpr int kThr = 640;
 constexpr uint32_t kBlk = kQ * 128;     // 16 KB: 128 rows of 64 bf16 columns
 
 // tensor memory columns
 constexpr uint32_t kTG = 0;             // G, 128
 constexpr uint32_t kTP = 128;           // P as bf16 pairs, 64
-constexpr uint32_t kTD = 192;           // dS of the three parts of W V, 64 each
+constexpr uint32_t kTD = 192;           // dS: first part of W V, then the two others, 64 each
+constexpr uint32_t kTS = 320;           // S^T fp32, 64
 constexpr uint32_t kTY1 = 384;
 constexpr uint32_t kTY2 = 448;
 
-constexpr int kScFloats = 356;          // loc[128], dt[128], colf[96], block sums[4]
+constexpr int kScFloats = 260;          // suf[128], dt[128], block sums[4]
 
 template <int KB>                       // 64-column blocks of d_k
 struct Lay {
   static constexpr int NST = KB == 2 ? 2 : 3;              // stages
-  static constexpr uint32_t kK = 0;                        // keys, then queries, then values
-  static constexpr uint32_t kQr = KB * kBlk;
-  static constexpr uint32_t kV = 2 * KB * kBlk;
-  static constexpr uint32_t kStage = (2 * KB + 1) * kBlk;
-  static constexpr uint32_t kXw = NST * kStage;            // W V: three parts
+  static constexpr uint32_t kQr = KB * kBlk;               // keys, then queries
+  static constexpr uint32_t kKQ = 2 * KB * kBlk;           // one stage of both
+  static constexpr uint32_t kV = NST * kKQ;                // values, then y
+  static constexpr uint32_t kXw = kV + NST * kBlk;         // W V: three parts
   static constexpr uint32_t kS = kXw + 3 * kBlk;           // state copy [64 KB rows][64 columns]
   static constexpr uint32_t kSc = kS + KB * 8192;          // scalars per stage
   static constexpr uint32_t kBar = kSc + NST * kScFloats * 4;
-  static constexpr int kNBar = 3 * NST + 11;
+  static constexpr int kNBar = 6 * NST + 11;
   static constexpr uint32_t kBytes = kBar + kNBar * 8 + 16;
 };
 static_assert(Lay<1>::kBar % 8 == 0 && Lay<2>::kBar % 8 == 0, "mbarriers");
@@ -83,18 +84,24 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// 32 consecutive columns of this thread's tensor-memory lane; the wait comes with tmem_ld_wait.
-__device__ __forceinline__ void tmem_ld32_raw(uint32_t t, uint32_t (&r)[32]) {
+// Two loads of 16 columns of this thread's tensor-memory lane, one wait.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, uint32_t (&x)[16],
+                                            uint32_t (&y)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(t)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]),
+        "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3]), "=r"(y[4]), "=r"(y[5]), "=r"(y[6]), "=r"(y[7]), "=r"(y[8]), "=r"(y[9]), "=r"(y[10]), "=r"(y[11]), "=r"(y[12]), "=r"(y[13]), "=r"(y[14]), "=r"(y[15])
+      : "r"(ta), "r"(tb)
+      : "memory");
+}
+
+// 8 consecutive columns of this thread's lane.
+__device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
       : "memory");
 }
 
@@ -132,31 +139,34 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// Barrier over `count` threads that returns the AND of `v` over them: a group of warps whose waits
-// may run out leaves its loop together.
-__device__ __forceinline__ bool bar_and(int id, int count, bool v) {
-  uint32_t out;
+// Three loads of 8 columns, one wait.
+__device__ __forceinline__ void tmem_ld8x3(uint32_t ta, uint32_t tb, uint32_t tc, float (&x)[24]) {
+  uint32_t r[24];
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(out)
-      : "r"(uint32_t(v)), "r"(id), "r"(count)
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%24];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%25];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%26];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23])
+      : "r"(ta), "r"(tb), "r"(tc)
       : "memory");
-  return out != 0;
+#pragma unroll
+  for (int j = 0; j < 24; ++j) x[j] = __uint_as_float(r[j]);
 }
 
-template <int KB, bool FULL>
+template <int KB, bool FULL, bool GATE>
 __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_constant__ ChunkScan c) {
   using Y = Lay<KB>;
   constexpr int NST = Y::NST;
   extern __shared__ __align__(1024) unsigned char sm[];
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Y::kBar);
-  uint64_t* full = bar;                  // [NST] tiles landed (TMA bytes)
-  uint64_t* empty = bar + NST;           // [NST] stage and scalars reusable
-  uint64_t* sc_full = bar + 2 * NST;     // [NST] scalars written (4 warps)
-  uint64_t* one = bar + 3 * NST;
+  uint64_t* kq_full = bar;               // [NST] keys and queries landed (TMA bytes)
+  uint64_t* kq_free = bar + NST;         // [NST] ... read by the products (commit)
+  uint64_t* v_full = bar + 2 * NST;      // [NST] values landed (TMA bytes)
+  uint64_t* v_done = bar + 3 * NST;      // [NST] y written over them (4 warps); dS done if !FULL
+  uint64_t* sc_full = bar + 4 * NST;     // [NST] scalars written
+  uint64_t* sc_free = bar + 5 * NST;     // [NST] scalars read (commit, 4 state and 4 output warps)
+  uint64_t* one = bar + 6 * NST;
   uint64_t* xw_full = one + 0;           // W V written (4 warps)
   uint64_t* ds_full = one + 1;           // dS done (and W V read)
   uint64_t* ds_free = one + 2;           // dS read (4 warps)
@@ -189,10 +199,12 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   }
   if (tid == 0) {
     for (int s = 0; s < NST; ++s) {
-      mbar_init(&full[s], 1);
-      // MMA commit, state warps, and the block of output warps
-      mbar_init(&empty[s], FULL ? 6 : 5);
-      mbar_init(&sc_full[s], 4);
+      mbar_init(&kq_full[s], 1);
+      mbar_init(&kq_free[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_done[s], FULL ? 4 : 1);
+      mbar_init(&sc_full[s], 1);
+      mbar_init(&sc_free[s], FULL ? 9 : 5);
     }
     mbar_init(xw_full, 4);
     mbar_init(ds_full, 1);
@@ -213,113 +225,207 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   tc_fence_after();
   const uint32_t tmem = *holder;
   const uint32_t base = smem_u32(sm);
+  const float* scal = reinterpret_cast<const float*>(sm + Y::kSc);
 
-  if (warp == 16) {
-    // ------------------------------------------------------------------ TMA loads
-    if (lane == 0) {
-      prefetch_tmap(&c.mk);
-      prefetch_tmap(&c.mv);
-      if (FULL) prefetch_tmap(&c.mq);
-      constexpr uint32_t bytes = (FULL ? 2 * KB + 1 : KB + 1) * kBlk;
-      int issued = 0;
+  if (warp >= 16) {
+    if (warp == 16) {
+      // ---------------------------------------------------------------- keys and queries
+      if (lane == 0) {
+        prefetch_tmap(&c.mk);
+        if (FULL) prefetch_tmap(&c.mq);
+        int issued = 0;
+        for (int i = 0; i < nch; ++i) {
+          const int s = i % NST, n = i / NST;
+          if (n > 0 && !mbar_wait_bounded(&kq_free[s], (n - 1) & 1)) {
+            report_error(a.err, OLA_ERR_TIMEOUT, 60, i);
+            break;
+          }
+          mbar_arrive_expect_tx(&kq_full[s], (FULL ? 2 : 1) * KB * kBlk);
+          unsigned char* st = sm + s * Y::kKQ;
+          const int p = p0 + i * kQ;
+#pragma unroll
+          for (int b = 0; b < KB; ++b) {
+            tma_load_4d(st + b * kBlk, &c.mk, &kq_full[s], 64 * b, g, p, r);
+            if (FULL) tma_load_4d(st + Y::kQr + b * kBlk, &c.mq, &kq_full[s], 64 * b, g, p, r);
+          }
+          issued = i + 1;
+        }
+        // the copies still in flight land before the block exits
+        for (int i = issued > NST ? issued - NST : 0; i < issued; ++i)
+          mbar_wait_bounded(&kq_full[i % NST], (i / NST) & 1);
+      }
+      __syncwarp();
+    } else if (warp == 17) {
+      // ---------------------------------------------------------------- products
+      const uint32_t id_g = idesc_bf16_f32(128, 128);
+      const uint32_t id_y = idesc_bf16_f32(128, kNV) | (1u << 16);               // B MN-major
+      const uint32_t id_d2 = idesc_bf16_f32_amn(128, 2 * kNV) | (1u << 16);      // A, B MN-major
+      const uint32_t id_d1 = idesc_bf16_f32_amn(128, kNV) | (1u << 16);
+      auto issue_g = [&](int i) -> bool {
+        const int s = i % NST;
+        if (!warp_wait(&kq_full[s], i / NST) || (i > 0 && !warp_wait(g_free, i - 1)))
+          return false;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t dk = sw128_kmajor_desc(base + s * Y::kKQ);
+          const uint64_t dq = sw128_kmajor_desc(base + s * Y::kKQ + Y::kQr);
+#pragma unroll
+          for (int k = 0; k < 4 * KB; ++k) {
+            const uint64_t off = (k >> 2) * (kBlk >> 4) + (k & 3) * 2;
+            umma_bf16(tmem + kTG, dq + off, dk + off, id_g, k != 0);
+          }
+          umma_commit(g_full);
+        }
+        __syncwarp();
+        return true;
+      };
+      bool ok = !FULL || nch == 0 || issue_g(0);
+      for (int i = 0; i < nch && ok; ++i) {
+        const int s = i % NST;
+        // dS: A = keys read MN-major (key columns along M; for d_k <= 64 the upper 64 rows read
+        // the next tile and are not used), B = the first two parts of W V side by side; the third is added
+        // to the second
+        ok = warp_wait(&kq_full[s], i / NST) && warp_wait(xw_full, i) &&
+             (i == 0 || warp_wait(ds_free, i - 1));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t dk = sw128_mnmajor_desc(base + s * Y::kKQ, kBlk, 1024);
+          const uint64_t dx = sw128_mnmajor_desc(base + Y::kXw, kBlk, 1024);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            umma_bf16(tmem + kTD, dk + k * 128, dx + k * 128, id_d2, k != 0);
+            umma_bf16(tmem + kTD + kNV, dk + k * 128, dx + (2 * kBlk >> 4) + k * 128, id_d1, 1u);
+          }
+          umma_commit(ds_full);
+          if (!FULL) {
+            umma_commit(&kq_free[s]);
+            umma_commit(&v_done[s]);
+            umma_commit(&sc_free[s]);
+          }
+        }
+        __syncwarp();
+        if (!FULL) continue;
+        // Y2: A = queries, B = the state copy (rows = key columns)
+        ok = warp_wait(s_full, i) && (i == 0 || warp_wait(y_free, i - 1));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t dq = sw128_kmajor_desc(base + s * Y::kKQ + Y::kQr);
+          const uint64_t dsd = sw128_mnmajor_desc(base + Y::kS, kBlk, 1024);
+#pragma unroll
+          for (int k = 0; k < 4 * KB; ++k)
+            umma_bf16(tmem + kTY2, dq + (k >> 2) * (kBlk >> 4) + (k & 3) * 2, dsd + k * 128, id_y,
+                      k != 0);
+          umma_commit(s_free);
+          umma_commit(&kq_free[s]);
+        }
+        __syncwarp();
+        if (i + 1 < nch && !(ok = issue_g(i + 1))) break;
+        // Y1: A = P in tensor memory, B = the values (rows = tokens)
+        ok = warp_wait(&v_full[s], i / NST) && warp_wait(p_full, i);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t dv = sw128_mnmajor_desc(base + Y::kV + s * kBlk, kBlk, 1024);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            umma_bf16_ts(tmem + kTY1, tmem + kTP + k * 8, dv + k * 128, id_y, k != 0);
+          umma_commit(y_full);
+          umma_commit(&sc_free[s]);
+        }
+        __syncwarp();
+      }
+      if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 61, 0);
+      if (elect_one()) umma_commit(done);
+      __syncwarp();
+      mbar_wait_bounded(done, 0);              // before tensor memory is released
+      __syncwarp();
+    } else if (warp == 18) {
+      // ---------------------------------------------------------------- values in, y out
+      if (lane == 0) {
+        prefetch_tmap(&c.mv);
+        auto load = [&](int i) {
+          const int s = i % NST;
+          mbar_arrive_expect_tx(&v_full[s], kBlk);
+          tma_load_4d(sm + Y::kV + s * kBlk, &c.mv, &v_full[s], kNV * tile, h, p0 + i * kQ, r);
+        };
+        int issued = 0;
+        for (; issued < nch && issued < NST; ++issued) load(issued);
+        for (int i = 0; i < nch; ++i) {
+          const int s = i % NST;
+          if (!mbar_wait_bounded(&v_done[s], (i / NST) & 1)) {
+            report_error(a.err, OLA_ERR_TIMEOUT, 66, i);
+            break;
+          }
+          // rows past P are clipped; a sequence that ends inside the chunk but before P was
+          // stored row by row
+          if (FULL && (p0 + (i + 1) * kQ <= p1 || p1 == a.P)) {
+            tma_store_4d(&c.my, sm + Y::kV + s * kBlk, kNV * tile, h, p0 + i * kQ, r);
+            bulk_commit();
+            bulk_wait_read();
+          }
+          if (issued < nch) load(issued++);
+        }
+        for (int i = issued > NST ? issued - NST : 0; i < issued; ++i)
+          mbar_wait_bounded(&v_full[i % NST], (i / NST) & 1);
+        bulk_wait_all();
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------------- scalars
+      // lane = 4 tokens, 8 lanes = a block of 32; every sum runs over tokens behind the token
+      const float A2 = a.A[h] * 1.4426950408889634f;
+      const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+      const float* dtp = a.dt + int64_t(r) * a.P * a.H + h;
+      float raw[4];
+      auto load_dt = [&](int i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int p = p0 + i * kQ + 4 * lane + e;
+          raw[e] = i < nch && p < p1 ? __ldg(dtp + int64_t(p) * a.H) : 0.f;
+        }
+      };
+      load_dt(0);
       for (int i = 0; i < nch; ++i) {
         const int s = i % NST, n = i / NST;
-        if (n > 0 && !mbar_wait_bounded(&empty[s], (n - 1) & 1)) {
-          report_error(a.err, OLA_ERR_TIMEOUT, 60, i);
+        const int left = p1 - (p0 + i * kQ);            // tokens of the piece from here on
+        float dt[4], sf[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // tokens behind the end take no part: dt = 0
+          dt[e] = raw[e] + bias;
+          if (a.softplus) dt[e] = softplus_f(dt[e]);
+          if (4 * lane + e >= left) dt[e] = 0.f;
+        }
+        load_dt(i + 1);
+        // a decay below 2^-256 is 0; the clamp keeps sums of resets finite
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 3; e >= 0; --e) {
+          sf[e] = sum;
+          sum += fmaxf(dt[e] * A2, -256.f);
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+          const float d = __shfl_down_sync(kFull, sum, o);
+          if ((lane & 7) + o < 8) sum += d;
+        }
+        float behind = __shfl_down_sync(kFull, sum, 1);
+        if ((lane & 7) == 7) behind = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sf[e] += behind;
+        if (n > 0 && !warp_wait(&sc_free[s], n - 1)) {
+          if (lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 67, i);
           break;
         }
-        mbar_arrive_expect_tx(&full[s], bytes);
-        unsigned char* st = sm + s * Y::kStage;
-        const int p = p0 + i * kQ;
-#pragma unroll
-        for (int b = 0; b < KB; ++b) {
-          tma_load_4d(st + Y::kK + b * kBlk, &c.mk, &full[s], 64 * b, g, p, r);
-          if (FULL) tma_load_4d(st + Y::kQr + b * kBlk, &c.mq, &full[s], 64 * b, g, p, r);
-        }
-        tma_load_4d(st + Y::kV, &c.mv, &full[s], kNV * tile, h, p, r);
-        issued = i + 1;
+        float4* out = reinterpret_cast<float4*>(sm + Y::kSc + s * kScFloats * 4);
+        out[lane] = make_float4(sf[0], sf[1], sf[2], sf[3]);
+        out[32 + lane] = make_float4(dt[0], dt[1], dt[2], dt[3]);
+        if ((lane & 7) == 0) reinterpret_cast<float*>(out + 64)[lane >> 3] = sum;
+        warp_arrive(&sc_full[s]);
       }
-      // the copies still in flight land before the block exits
-      for (int i = issued > NST ? issued - NST : 0; i < issued; ++i)
-        mbar_wait_bounded(&full[i % NST], (i / NST) & 1);
     }
-  } else if (warp == 17) {
-    // ------------------------------------------------------------------ products
-    const uint32_t id_g = idesc_bf16_f32(128, 128);
-    const uint32_t id_y = idesc_bf16_f32(128, kNV) | (1u << 16);               // B MN-major
-    const uint32_t id_d = idesc_bf16_f32_amn(128, 3 * kNV) | (1u << 16);       // A, B MN-major
-    auto issue_g = [&](int i) -> bool {
-      const int s = i % NST;
-      if (!warp_wait(&full[s], i / NST) || (i > 0 && !warp_wait(g_free, i - 1))) return false;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t dq = sw128_kmajor_desc(base + s * Y::kStage + Y::kQr);
-        const uint64_t dk = sw128_kmajor_desc(base + s * Y::kStage + Y::kK);
-#pragma unroll
-        for (int k = 0; k < 4 * KB; ++k) {
-          const uint64_t off = (k >> 2) * (kBlk >> 4) + (k & 3) * 2;
-          umma_bf16(tmem + kTG, dq + off, dk + off, id_g, k != 0);
-        }
-        umma_commit(g_full);
-      }
-      __syncwarp();
-      return true;
-    };
-    bool ok = !FULL || nch == 0 || issue_g(0);
-    for (int i = 0; i < nch && ok; ++i) {
-      const int s = i % NST;
-      const uint32_t st = base + s * Y::kStage;
-      // dS: A = keys read MN-major (key columns along M; for d_k <= 64 the upper 64 rows read the
-      // next tile and are not used), B = the three parts of W V side by side
-      ok = warp_wait(&full[s], i / NST) && warp_wait(xw_full, i) &&
-           (i == 0 || warp_wait(ds_free, i - 1));
-      if (!ok) break;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t dk = sw128_mnmajor_desc(st + Y::kK, kBlk, 1024);
-        const uint64_t dx = sw128_mnmajor_desc(base + Y::kXw, kBlk, 1024);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          umma_bf16(tmem + kTD, dk + k * 128, dx + k * 128, id_d, k != 0);
-        umma_commit(ds_full);
-        if (!FULL) umma_commit(&empty[s]);
-      }
-      __syncwarp();
-      if (!FULL) continue;
-      // Y2: A = queries, B = the state copy (rows = key columns)
-      ok = warp_wait(s_full, i) && (i == 0 || warp_wait(y_free, i - 1));
-      if (!ok) break;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t dq = sw128_kmajor_desc(st + Y::kQr);
-        const uint64_t dsd = sw128_mnmajor_desc(base + Y::kS, kBlk, 1024);
-#pragma unroll
-        for (int k = 0; k < 4 * KB; ++k)
-          umma_bf16(tmem + kTY2, dq + (k >> 2) * (kBlk >> 4) + (k & 3) * 2, dsd + k * 128, id_y,
-                    k != 0);
-        umma_commit(s_free);
-      }
-      __syncwarp();
-      if (i + 1 < nch && !(ok = issue_g(i + 1))) break;
-      // Y1: A = P in tensor memory, B = the values (rows = tokens)
-      ok = warp_wait(p_full, i);
-      if (!ok) break;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t dv = sw128_mnmajor_desc(st + Y::kV, kBlk, 1024);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          umma_bf16_ts(tmem + kTY1, tmem + kTP + k * 8, dv + k * 128, id_y, k != 0);
-        umma_commit(y_full);
-        umma_commit(&empty[s]);
-      }
-      __syncwarp();
-    }
-    if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 61, 0);
-    if (elect_one()) umma_commit(done);
-    __syncwarp();
-    mbar_wait_bounded(done, 0);              // before tensor memory is released
-    __syncwarp();
   } else if (warp < 4) {
     // ------------------------------------------------------------------ G -> P
     if (FULL) {
@@ -338,49 +444,37 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
              (i == 0 || warp_wait(y_full, i - 1));
         if (!ok) break;
         tc_fence_after();
-        const float* loc = reinterpret_cast<const float*>(sm + Y::kSc) + s * kScFloats;
-        const float* dts = loc + 128;
-        const float* colf = loc + 256;
-        const float* bs = loc + 352;
-        const float mine = loc[t];
-        float mid = mine;                    // log2 decay from the end of block j to t
+        const float* suf = scal + s * kScFloats;
+        const float* dts = suf + 128;
+        const float* bs = suf + 256;
+        // log2 decay from the end of block j to t; in t's own block its negative complement, so
+        // that mid + suf[s] is the decay from s to t in every block
+        float mid = -suf[t];
 #pragma unroll 1
-        for (int j = warp; j >= 0; --j) {
-          uint32_t x[32];
-          tmem_ld32_raw(tl + kTG + 32 * j, x);
-          uint32_t p[16];
-          if (j == warp) {
+        for (int jj = 0; jj < 2 * (warp + 1); ++jj) {
+          const int j = warp - (jj >> 1), col = 32 * j + 16 * (jj & 1), lim = t - col;
+          float4 l4[4], d4[4];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 l4 = *reinterpret_cast<const float4*>(loc + 32 * j + 4 * q);
-              const float4 d4 = *reinterpret_cast<const float4*>(dts + 32 * j + 4 * q);
-              const float lv[4] = {l4.x, l4.y, l4.z, l4.w}, dv[4] = {d4.x, d4.y, d4.z, d4.w};
-              float f[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                f[e] = 4 * q + e <= lane
-                           ? __uint_as_float(x[4 * q + e]) * (ex2(mine - lv[e]) * dv[e])
-                           : 0.f;
-              p[2 * q] = pack2(f[0], f[1]);
-              p[2 * q + 1] = pack2(f[2], f[3]);
-            }
-          } else {
-            const float rf = ex2(mid);
-            mid += bs[j];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 c4 = *reinterpret_cast<const float4*>(colf + 32 * j + 4 * q);
-              p[2 * q] = pack2(__uint_as_float(x[4 * q]) * (rf * c4.x),
-                               __uint_as_float(x[4 * q + 1]) * (rf * c4.y));
-              p[2 * q + 1] = pack2(__uint_as_float(x[4 * q + 2]) * (rf * c4.z),
-                                   __uint_as_float(x[4 * q + 3]) * (rf * c4.w));
-            }
+          for (int q = 0; q < 4; ++q) {
+            l4[q] = *reinterpret_cast<const float4*>(suf + col + 4 * q);
+            d4[q] = *reinterpret_cast<const float4*>(dts + col + 4 * q);
           }
-          uint4 v4[4];
+          float x[16];
+          tmem_ld16(tl + kTG + col, x);
+          uint32_t p[8];
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            v4[q] = make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
-          tmem_st16(tl + kTP + 16 * j, v4);
+          for (int q = 0; q < 4; ++q) {
+            const float lv[4] = {l4[q].x, l4[q].y, l4[q].z, l4[q].w};
+            const float dv[4] = {d4[q].x, d4[q].y, d4[q].z, d4[q].w};
+            float f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              f[e] = 4 * q + e <= lim ? x[4 * q + e] * (ex2(mid + lv[e]) * dv[e]) : 0.f;
+            p[2 * q] = pack2(f[0], f[1]);
+            p[2 * q + 1] = pack2(f[2], f[3]);
+          }
+          tmem_st8(tl + kTP + (col >> 1), p);
+          if (jj & 1) mid += bs[j];
         }
         tmem_st_wait();
         tc_fence_before();
@@ -393,80 +487,53 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 62, 0);
     }
   } else if (warp < 8) {
-    // ------------------------------------------------------------------ scalars and W V
+    // ------------------------------------------------------------------ W V
     const int t = tid - 128, w4 = warp - 4;
-    const float A2 = a.A[h] * 1.4426950408889634f;
-    const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
-    const float* dtp = a.dt + int64_t(r) * a.P * a.H + h;
-    auto load_dt = [&](int i) -> float {
-      const int p = p0 + i * kQ + t;
-      return i < nch && p < p1 ? __ldg(dtp + int64_t(p) * a.H) : 0.f;
-    };
-    float raw = load_dt(0);
     bool ok = true;
     for (int i = 0; i < nch; ++i) {
       const int s = i % NST, n = i / NST;
-      const int left = p1 - (p0 + i * kQ);              // tokens of the piece from here on
-      // tokens behind the end take no part: dt = 0
-      float dt = raw + bias;
-      if (a.softplus) dt = softplus_f(dt);
-      if (t >= left) dt = 0.f;
-      raw = load_dt(i + 1);
-      // a decay below 2^-256 is 0; the clamp keeps sums of resets finite
-      const float g2 = fmaxf(dt * A2, -256.f);
-      float pre = g2, suf = g2;                          // inclusive sums over the warp's 32 tokens
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float u = __shfl_up_sync(kFull, pre, o), d = __shfl_down_sync(kFull, suf, o);
-        if (lane >= o) pre += u;
-        if (lane + o < 32) suf += d;
-      }
-      float after = __shfl_down_sync(kFull, suf, 1);     // tokens of the block behind t
-      if (lane == 31) after = 0.f;
-      ok = ok && (n == 0 || warp_wait(&empty[s], n - 1));
-      float* loc = reinterpret_cast<float*>(sm + Y::kSc) + s * kScFloats;
-      if (ok) {
-        loc[t] = pre;
-        loc[128 + t] = dt;
-        if (w4 < 3) loc[256 + t] = dt * ex2(after);
-        if (lane == 31) loc[352 + w4] = pre;
-      }
-      if (!(ok = bar_and(1, 128, ok))) break;
-      if (lane == 0) mbar_arrive(&sc_full[s]);
-      for (int j = w4 + 1; j < 4; ++j) after += loc[352 + j];
-      const float w = dt * exp2f(after);
-      // (a wait that ran out is acted on at the next barrier of the four warps)
-      ok = warp_wait(&full[s], n) && (i == 0 || warp_wait(ds_full, i - 1));
-      if (!ok) continue;
-      unsigned char* vrow = sm + s * Y::kStage + Y::kV + t * 128;
+      const int left = p1 - (p0 + i * kQ);
+      ok = warp_wait(&sc_full[s], n);
+      if (!ok) break;
+      const float* suf = scal + s * kScFloats;
+      float after = suf[t];
+      for (int j = w4 + 1; j < 4; ++j) after += suf[256 + j];
+      const float w = suf[128 + t] * exp2f(after);
+      ok = warp_wait(&v_full[s], n) && (i == 0 || warp_wait(ds_full, i - 1));
+      if (!ok) break;
+      unsigned char* vrow = sm + Y::kV + s * kBlk + t * 128;
       unsigned char* xrow = sm + Y::kXw + t * 128;
-      if (t >= left) {
+      if (left < kQ) {
         // padding may hold anything, also NaN: its key and value rows are cleared
-        const uint4 z = make_uint4(0, 0, 0, 0);
+        ok = warp_wait(&kq_full[s], n);
+        if (!ok) break;
+        if (t >= left) {
+          const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+          for (int q = 0; q < 8; ++q) {
+            reinterpret_cast<uint4*>(vrow)[q] = z;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          reinterpret_cast<uint4*>(vrow)[q] = z;
-#pragma unroll
-          for (int b = 0; b < KB; ++b)
-            reinterpret_cast<uint4*>(sm + s * Y::kStage + Y::kK + b * kBlk + t * 128)[q] = z;
+            for (int b = 0; b < KB; ++b)
+              reinterpret_cast<uint4*>(sm + s * Y::kKQ + b * kBlk + t * 128)[q] = z;
+          }
         }
       }
-#pragma unroll 2
+      // a product of 24 bits is its upper 8 bits, the next 8 and the rest, each cut off exactly
+      uint4 nx = *reinterpret_cast<const uint4*>(vrow + ((t & 7) << 4));
+#pragma unroll 1
       for (int q = 0; q < 8; ++q) {
         const uint32_t off = uint32_t((q ^ (t & 7)) << 4);
-        const uint4 v4 = *reinterpret_cast<const uint4*>(vrow + off);
-        const uint32_t vw[4] = {v4.x, v4.y, v4.z, v4.w};
+        const uint32_t vw[4] = {nx.x, nx.y, nx.z, nx.w};
+        nx = *reinterpret_cast<const uint4*>(vrow + ((((q + 1) & 7) ^ (t & 7)) << 4));
         uint32_t h1[4], h2[4], h3[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float f0 = lo_f(vw[e]) * w, f1 = hi_f(vw[e]) * w;
-          h1[e] = pack2(f0, f1);
-          f0 -= lo_f(h1[e]);
-          f1 -= hi_f(h1[e]);
-          h2[e] = pack2(f0, f1);
-          f0 -= lo_f(h2[e]);
-          f1 -= hi_f(h2[e]);
-          h3[e] = pack2(f0, f1);
+          const float f0 = lo_f(vw[e]) * w, f1 = hi_f(vw[e]) * w;
+          h1[e] = __byte_perm(__float_as_uint(f0), __float_as_uint(f1), 0x7632);
+          const float r0 = f0 - hi_f(__float_as_uint(f0)), r1 = f1 - hi_f(__float_as_uint(f1));
+          h2[e] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
+          const float u0 = r0 - hi_f(__float_as_uint(r0)), u1 = r1 - hi_f(__float_as_uint(r1));
+          h3[e] = __byte_perm(__float_as_uint(u0), __float_as_uint(u1), 0x7632);
         }
         *reinterpret_cast<uint4*>(xrow + off) = make_uint4(h1[0], h1[1], h1[2], h1[3]);
         *reinterpret_cast<uint4*>(xrow + kBlk + off) = make_uint4(h2[0], h2[1], h2[2], h2[3]);
@@ -486,58 +553,68 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       entering = a.nseg > 1 ? a.seg_S + (int64_t(rh) * a.nseg + seg) * a.d_v * a.d_k
                             : (a.S_in ? a.S_in + int64_t(rh) * a.d_v * a.d_k : nullptr);
     const int v0 = kNV * tile, nv = min(kNV, a.d_v - v0);
-    float S[kNV];
+    unsigned char* row = sm + Y::kS + k * 128;             // the copy: 64 columns, 128-byte swizzle
+    auto copy8 = [&](int q, const uint32_t (&x)[8]) {
+      if (holds)
+        *reinterpret_cast<uint4*>(row + ((q ^ (k & 7)) << 4)) =
+            make_uint4(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                       pack2(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                       pack2(__uint_as_float(x[4]), __uint_as_float(x[5])),
+                       pack2(__uint_as_float(x[6]), __uint_as_float(x[7])));
+    };
+#pragma unroll 1
+    for (int q = 0; q < 8; ++q) {
+      uint32_t x[8];
 #pragma unroll
-    for (int v = 0; v < kNV; ++v)
-      S[v] = entering && mine && v < nv ? entering[int64_t(v0 + v) * a.d_k + k] : 0.f;
-    // the bf16 copy: row k of 64 value columns, 128-byte swizzle
-    auto copy_out = [&]() {
-      if (holds) {
-        unsigned char* row = sm + Y::kS + k * 128;
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<uint4*>(row + ((q ^ (k & 7)) << 4)) =
-              make_uint4(pack2(S[8 * q], S[8 * q + 1]), pack2(S[8 * q + 2], S[8 * q + 3]),
-                         pack2(S[8 * q + 4], S[8 * q + 5]), pack2(S[8 * q + 6], S[8 * q + 7]));
-      }
+      for (int e = 0; e < 8; ++e)
+        x[e] = entering && mine && 8 * q + e < nv
+                   ? __float_as_uint(entering[int64_t(v0 + 8 * q + e) * a.d_k + k])
+                   : 0u;
+      tmem_st8(tl + kTS + 8 * q, x);
+      if (FULL) copy8(q, x);
+    }
+    tmem_st_wait();
+    if (FULL) {
       fence_proxy_async_smem();
       warp_arrive(s_full);
-    };
-    if (FULL && nch > 0) copy_out();
+    }
     double logsum = 0.0;
     bool ok = true;
     for (int i = 0; i < nch; ++i) {
       const int s = i % NST;
-      ok = warp_wait(&sc_full[s], i / NST) && warp_wait(ds_full, i);
+      ok = warp_wait(&sc_full[s], i / NST);
       if (!ok) break;
-      tc_fence_after();
-      const float4 b4 = *reinterpret_cast<const float4*>(
-          reinterpret_cast<const float*>(sm + Y::kSc) + s * kScFloats + 352);
+      const float4 b4 = *reinterpret_cast<const float4*>(scal + s * kScFloats + 256);
       const float total = (b4.x + b4.y) + (b4.z + b4.w);
-      warp_arrive(&empty[s]);
+      warp_arrive(&sc_free[s]);
       if (!FULL) logsum += double(total);
       // e^{c_C} S as S + (e^{c_C} - 1) S where the decay is slow, so that it is not rounded chunk
       // after chunk; a fast decay would cancel in that form and is taken as it is
-      const float x = total * 0.69314718055994531f;
-      const bool slow = x > -0.5f;
-      const float mul = slow ? expm1f(x) : expf(x);
-#pragma unroll
+      const float ex = total * 0.69314718055994531f;
+      const bool slow = ex > -0.5f;
+      const float mul = slow ? expm1f(ex) : expf(ex);
+      const float keep = slow ? 1.f : 0.f;
+      ok = warp_wait(ds_full, i) && (!FULL || warp_wait(s_free, i));
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll 1
       for (int q = 0; q < 8; ++q) {
-        float x0[8], x1[8], x2[8], x3[8];
-        // (the fourth load repeats the third: one wait for all)
-        tmem_ld8x4(tl + kTD + 8 * q, tl + kTD + 64 + 8 * q, tl + kTD + 128 + 8 * q,
-                   tl + kTD + 128 + 8 * q, x0, x1, x2, x3);
+        float d[24];
+        tmem_ld8x3(tl + kTD + 8 * q, tl + kTD + kNV + 8 * q, tl + kTS + 8 * q, d);
+        uint32_t x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float own = x0[e] + (x1[e] + x2[e]), old = S[8 * q + e];
-          S[8 * q + e] = fmaf(mul, old, slow ? old + own : own);
-        }
+        for (int e = 0; e < 8; ++e)
+          x[e] = __float_as_uint(fmaf(mul, d[16 + e], fmaf(keep, d[16 + e], d[e] + d[8 + e])));
+        tmem_st8(tl + kTS + 8 * q, x);
+        if (FULL) copy8(q, x);
       }
+      tmem_st_wait();
       tc_fence_before();
-      warp_arrive(ds_free);
-      if (FULL && i + 1 < nch) {
-        if (!(ok = warp_wait(s_free, i))) break;
-        copy_out();
+      if (FULL) fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(ds_free);
+        if (FULL) mbar_arrive(s_full);
       }
     }
     if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 64, 0);
@@ -546,10 +623,15 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       out = a.seg_S + (int64_t(rh) * a.nseg + seg) * a.d_v * a.d_k;
     else if (seg == nseg - 1 && a.S_out)
       out = a.S_out + int64_t(rh) * a.d_v * a.d_k;
-    if (out && mine) {
+    if (out) {
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        float x[16];
+        tmem_ld16(tl + kTS + 16 * q, x);
 #pragma unroll
-      for (int v = 0; v < kNV; ++v)
-        if (v < nv) out[int64_t(v0 + v) * a.d_k + k] = S[v];
+        for (int e = 0; e < 16; ++e)
+          if (mine && 16 * q + e < nv) out[int64_t(v0 + 16 * q + e) * a.d_k + k] = x[e];
+      }
     }
     if (!FULL && tile == 0 && k == 0)
       a.seg_a[int64_t(rh) * a.nseg + seg] = float(exp2(logsum));
@@ -559,11 +641,12 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       const int t = tid - 384, w4 = warp - 12;
       const uint32_t tl = tmem + (uint32_t(32 * w4) << 16);
       const int v0 = kNV * tile, nv = min(kNV, a.d_v - v0);
-      const float D = a.D ? a.D[h] : 0.f;
+      const bool skip = a.D != nullptr;
+      const float D = skip ? a.D[h] : 0.f;
       const __nv_bfloat16* zp =
-          a.z ? static_cast<const __nv_bfloat16*>(a.z) + int64_t(r) * a.z_seq + int64_t(h) * a.d_v +
-                    v0
-              : nullptr;
+          GATE ? static_cast<const __nv_bfloat16*>(a.z) + int64_t(r) * a.z_seq +
+                     int64_t(h) * a.d_v + v0
+               : nullptr;
       __nv_bfloat16* yp = static_cast<__nv_bfloat16*>(a.y) + int64_t(r) * a.y_seq +
                           int64_t(h) * a.d_v + v0;
       bool ok = true;
@@ -571,56 +654,52 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         const int s = i % NST;
         const int p = p0 + i * kQ + t;
         const bool live = p < p1;
-        uint4 zr[8];
-        if (a.z) {
+        const uint4* zrow = reinterpret_cast<const uint4*>(GATE ? zp + int64_t(p) * a.z_tok : nullptr);
+        if (GATE && live) {
+          // the row's four sectors on their way to L1 while the products run
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            zr[q] = make_uint4(0, 0, 0, 0);
-            if (live && 8 * q < nv)
-              zr[q] = __ldg(reinterpret_cast<const uint4*>(zp + int64_t(p) * a.z_tok) + q);
-          }
+          for (int q = 0; q < 4; ++q)
+            if (16 * q < nv) asm volatile("prefetch.global.L1 [%0];" ::"l"(zrow + 2 * q));
         }
-        ok = warp_wait(&sc_full[s], i / NST) && warp_wait(y_full, i);
-        if (!bar_and(2, 128, ok)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const float* loc = reinterpret_cast<const float*>(sm + Y::kSc) + s * kScFloats;
-        float cum = loc[t];
-        for (int j = 0; j < w4; ++j) cum += loc[352 + j];
+        ok = warp_wait(&sc_full[s], i / NST);
+        if (!ok) break;
+        const float* suf = scal + s * kScFloats;
+        float cum = suf[256 + w4] - suf[t];
+        for (int j = 0; j < w4; ++j) cum += suf[256 + j];
         const float ec = ex2(cum);
-        unsigned char* vrow = sm + s * Y::kStage + Y::kV + t * 128;
-        // whole rows go out by TMA (rows past P are clipped); a sequence that ends inside the
-        // chunk but before P is stored row by row
+        warp_arrive(&sc_free[s]);
+        unsigned char* vrow = sm + Y::kV + s * kBlk + t * 128;
         const bool by_tma = p0 + (i + 1) * kQ <= p1 || p1 == a.P;
+        ok = warp_wait(y_full, i);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int hq = 0; hq < 4; ++hq) {                 // 16 columns, two 16-byte pieces of a row
+          uint4 z4[2], v4[2];
+          unsigned char* at[2];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t x1[32], x2[32];
-          tmem_ld32_raw(tl + kTY1 + 32 * half, x1);
-          tmem_ld32_raw(tl + kTY2 + 32 * half, x2);
-          if (half == 1) {
-            tc_fence_before();
-            warp_arrive(y_free);
+          for (int u = 0; u < 2; ++u) {
+            const int q = 2 * hq + u;
+            at[u] = vrow + ((q ^ (t & 7)) << 4);
+            z4[u] = v4[u] = make_uint4(0, 0, 0, 0);
+            if (GATE && live && 8 * q < nv) z4[u] = __ldg(zrow + q);
+            if (skip) v4[u] = *reinterpret_cast<const uint4*>(at[u]);
           }
+          uint32_t x1[16], x2[16];
+          tmem_ld16x2(tl + kTY1 + 16 * hq, tl + kTY2 + 16 * hq, x1, x2);
 #pragma unroll
-          for (int qq = 0; qq < 4; ++qq) {
-            const int q = 4 * half + qq;
-            unsigned char* at = vrow + ((q ^ (t & 7)) << 4);
-            const uint4 v4 = *reinterpret_cast<const uint4*>(at);
-            const uint32_t vw[4] = {v4.x, v4.y, v4.z, v4.w};
-            const uint32_t zw[4] = {zr[q].x, zr[q].y, zr[q].z, zr[q].w};
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t vw[4] = {v4[u].x, v4[u].y, v4[u].z, v4[u].w};
+            const uint32_t zw[4] = {z4[u].x, z4[u].y, z4[u].z, z4[u].w};
             uint32_t ow[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int at0 = 8 * qq + 2 * e;
-              float o0 = fmaf(ec, __uint_as_float(x2[at0]), __uint_as_float(x1[at0]));
-              float o1 = fmaf(ec, __uint_as_float(x2[at0 + 1]), __uint_as_float(x1[at0 + 1]));
-              if (a.D) {
-                o0 = fmaf(D, lo_f(vw[e]), o0);
-                o1 = fmaf(D, hi_f(vw[e]), o1);
-              }
-              if (a.z) {
+              const int b = 8 * u + 2 * e;
+              float o0 = fmaf(ec, __uint_as_float(x2[b]), __uint_as_float(x1[b]));
+              float o1 = fmaf(ec, __uint_as_float(x2[b + 1]), __uint_as_float(x1[b + 1]));
+              o0 = fmaf(D, lo_f(vw[e]), o0);
+              o1 = fmaf(D, hi_f(vw[e]), o1);
+              if (GATE) {
                 o0 *= silu_f<__nv_bfloat16>(lo_f(zw[e]));
                 o1 *= silu_f<__nv_bfloat16>(hi_f(zw[e]));
               }
@@ -628,23 +707,16 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
             }
             const uint4 o4 = make_uint4(ow[0], ow[1], ow[2], ow[3]);
             if (by_tma)
-              *reinterpret_cast<uint4*>(at) = o4;
-            else if (live && 8 * q < nv)
-              *(reinterpret_cast<uint4*>(yp + int64_t(p) * a.y_tok) + q) = o4;
+              *reinterpret_cast<uint4*>(at[u]) = o4;
+            else if (live && 8 * (2 * hq + u) < nv)
+              *(reinterpret_cast<uint4*>(yp + int64_t(p) * a.y_tok) + 2 * hq + u) = o4;
           }
         }
-        if (by_tma) fence_proxy_async_smem();
-        named_bar_sync(2, 128);               // nothing between the two barriers can run out
-        if (t == 0) {
-          if (by_tma) {
-            tma_store_4d(&c.my, sm + s * Y::kStage + Y::kV, v0, h, p0 + i * kQ, r);
-            bulk_commit();
-            bulk_wait_read();
-          }
-          mbar_arrive(&empty[s]);
-        }
+        tc_fence_before();
+        warp_arrive(y_free);
+        fence_proxy_async_smem();
+        warp_arrive(&v_done[s]);
       }
-      if (t == 0) bulk_wait_all();
       if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 65, 0);
     }
   }
@@ -700,21 +772,26 @@ cudaError_t run(const ChunkScan& c, cudaStream_t st) {
   constexpr uint32_t bytes = Lay<KB>::kBytes;
   static std::atomic<uint64_t> set{0};
   cudaError_t e = once_per_device(set, [&] {
-    cudaError_t x = cudaFuncSetAttribute(scan_chunk_kernel<KB, true>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    return x != cudaSuccess
-               ? x
-               : cudaFuncSetAttribute(scan_chunk_kernel<KB, false>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t x = cudaSuccess;
+    for (auto f : {scan_chunk_kernel<KB, true, true>, scan_chunk_kernel<KB, true, false>,
+                   scan_chunk_kernel<KB, false, false>})
+      if (x == cudaSuccess)
+        x = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return x;
   });
   if (e != cudaSuccess) return e;
   const int64_t chains = int64_t(c.a.R) * c.a.H * c.ntile;
   if (c.a.nseg > 1) {
-    scan_chunk_kernel<KB, false><<<unsigned(chains * (c.a.nseg - 1)), kThr, bytes, st>>>(c);
+    scan_chunk_kernel<KB, false, false>
+        <<<unsigned(chains * (c.a.nseg - 1)), kThr, bytes, st>>>(c);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((e = launch_scan_join(c.a, st)) != cudaSuccess) return e;
   }
-  scan_chunk_kernel<KB, true><<<unsigned(chains * c.a.nseg), kThr, bytes, st>>>(c);
+  const unsigned grid = unsigned(chains * c.a.nseg);
+  if (c.a.z)
+    scan_chunk_kernel<KB, true, true><<<grid, kThr, bytes, st>>>(c);
+  else
+    scan_chunk_kernel<KB, true, false><<<grid, kThr, bytes, st>>>(c);
   return cudaGetLastError();
 }
 
