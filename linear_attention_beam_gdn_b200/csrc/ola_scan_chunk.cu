@@ -18,12 +18,15 @@
 // factor per row and one per column.
 //
 // One block per (sequence, head, 64 value columns, piece), one per SM:
-//   warps 0-3    G -> P (thread = token t; P into tensor memory as the A operand of Y1)
-//   warps 4-7    W V (thread = token s)
-//   warps 8-11   state rows (thread = key column, 64 fp32 of S^T): S = e^{c_C} S + dS, its bf16 copy
-//   warps 12-15  outputs (thread = token t): Y1 + e^{c_t} Y2, D, gate; y staged over v
-//   warp 16      TMA loads of keys and queries;   warp 17  tcgen05.mma
-//   warp 18      TMA stores of y and loads of v;  warp 19  the chunk's scalars (dt, running sums)
+//   warps 0-7    G -> P (thread = token t, half of the columns; P into tensor memory as the A
+//                operand of Y1)
+//   warps 8-15   outputs (thread = token t, half of the columns): Y1 + e^{c_t} Y2, D, gate; y staged
+//                over v
+//   warps 16-19  W V (thread = token s)
+//   warps 20-23  state rows (thread = key column, S^T in tensor memory): S = e^{c_C} S + dS and its
+//                bf16 copy
+//   warp 24      TMA loads of keys and queries;   warp 25  tcgen05.mma
+//   warp 26      TMA stores of y and loads of v;  warp 27  the chunk's scalars (dt, running sums)
 // Nothing but Y2 waits for the state, so the products of a chunk overlap the conversions of its
 // neighbours. A piece of a cut sequence runs twice: dS alone first (FULL = false), then, once
 // scan_join_kernel has made the state before every piece, the outputs.
@@ -35,7 +38,7 @@ namespace {
 
 constexpr int kQ = 128;                 // tokens per chunk
 constexpr int kNV = 64;                 // value columns per block
-constexpr int kThr = 640;
+constexpr int kThr = 896;
 constexpr uint32_t kBlk = kQ * 128;     // 16 KB: 128 rows of 64 bf16 columns
 
 // tensor memory columns
@@ -46,7 +49,7 @@ constexpr uint32_t kTS = 320;           // S^T fp32, 64
 constexpr uint32_t kTY1 = 384;
 constexpr uint32_t kTY2 = 448;
 
-constexpr int kScFloats = 260;          // suf[128], dt[128], block sums[4]
+constexpr int kScFloats = 356;          // suf[128], dt[128], colf[96], block sums[4]
 
 template <int KB>                       // 64-column blocks of d_k
 struct Lay {
@@ -58,7 +61,7 @@ struct Lay {
   static constexpr uint32_t kS = kXw + 3 * kBlk;           // state copy [64 KB rows][64 columns]
   static constexpr uint32_t kSc = kS + KB * 8192;          // scalars per stage
   static constexpr uint32_t kBar = kSc + NST * kScFloats * 4;
-  static constexpr int kNBar = 6 * NST + 11;
+  static constexpr int kNBar = 6 * NST + 14;
   static constexpr uint32_t kBytes = kBar + kNBar * 8 + 16;
 };
 static_assert(Lay<1>::kBar % 8 == 0 && Lay<2>::kBar % 8 == 0, "mbarriers");
@@ -83,6 +86,42 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Two fp32 at a time (fma.rn.f32x2): half the instructions of the scalar forms.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t u2(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float2 un2(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2(uint64_t a) {
+  const float2 f = un2(a);
+  return pack2(f.x, f.y);
+}
 
 // Two loads of 16 columns of this thread's tensor-memory lane, one wait.
 __device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, uint32_t (&x)[16],
@@ -163,21 +202,22 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   uint64_t* kq_full = bar;               // [NST] keys and queries landed (TMA bytes)
   uint64_t* kq_free = bar + NST;         // [NST] ... read by the products (commit)
   uint64_t* v_full = bar + 2 * NST;      // [NST] values landed (TMA bytes)
-  uint64_t* v_done = bar + 3 * NST;      // [NST] y written over them (4 warps); dS done if !FULL
+  uint64_t* v_done = bar + 3 * NST;      // [NST] y written over them (8 warps); dS done if !FULL
   uint64_t* sc_full = bar + 4 * NST;     // [NST] scalars written
-  uint64_t* sc_free = bar + 5 * NST;     // [NST] scalars read (commit, 4 state and 4 output warps)
+  uint64_t* sc_free = bar + 5 * NST;     // [NST] scalars read (commit, 4 state and 8 output warps)
   uint64_t* one = bar + 6 * NST;
-  uint64_t* xw_full = one + 0;           // W V written (4 warps)
-  uint64_t* ds_full = one + 1;           // dS done (and W V read)
-  uint64_t* ds_free = one + 2;           // dS read (4 warps)
-  uint64_t* g_full = one + 3;            // G done
-  uint64_t* g_free = one + 4;            // G read (4 warps)
-  uint64_t* p_full = one + 5;            // P written (4 warps)
-  uint64_t* s_full = one + 6;            // state copy written (4 warps)
-  uint64_t* s_free = one + 7;            // Y2 done: state copy read
-  uint64_t* y_full = one + 8;            // Y1 and Y2 done (and P read)
-  uint64_t* y_free = one + 9;            // Y1 and Y2 read (4 warps)
-  uint64_t* done = one + 10;             // every MMA completed
+  uint64_t* xw_full = one + 0;           // [2] W V of 64 tokens written (2 warps)
+  uint64_t* xw_free = one + 2;           // [2] ... read by dS (commit)
+  uint64_t* ds_full = one + 4;           // dS done
+  uint64_t* ds_free = one + 5;           // dS read (4 warps)
+  uint64_t* g_full = one + 6;            // G done
+  uint64_t* g_free = one + 7;            // G read (8 warps)
+  uint64_t* p_full = one + 8;            // P written (8 warps)
+  uint64_t* s_full = one + 9;            // state copy written (4 warps)
+  uint64_t* s_free = one + 10;           // Y2 done: state copy read
+  uint64_t* y_full = one + 11;           // Y1 and Y2 done (and P read)
+  uint64_t* y_free = one + 12;           // Y1 and Y2 read (8 warps)
+  uint64_t* done = one + 13;             // every MMA completed
   uint32_t* holder = reinterpret_cast<uint32_t*>(bar + Y::kNBar);
   const ScanArgs& a = c.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -202,24 +242,27 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       mbar_init(&kq_full[s], 1);
       mbar_init(&kq_free[s], 1);
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_done[s], FULL ? 4 : 1);
+      mbar_init(&v_done[s], FULL ? 8 : 1);
       mbar_init(&sc_full[s], 1);
-      mbar_init(&sc_free[s], FULL ? 9 : 5);
+      mbar_init(&sc_free[s], FULL ? 13 : 5);
     }
-    mbar_init(xw_full, 4);
+    for (int u = 0; u < 2; ++u) {
+      mbar_init(&xw_full[u], 2);
+      mbar_init(&xw_free[u], 1);
+    }
     mbar_init(ds_full, 1);
     mbar_init(ds_free, 4);
     mbar_init(g_full, 1);
-    mbar_init(g_free, 4);
-    mbar_init(p_full, 4);
+    mbar_init(g_free, 8);
+    mbar_init(p_full, 8);
     mbar_init(s_full, 4);
     mbar_init(s_free, 1);
     mbar_init(y_full, 1);
-    mbar_init(y_free, 4);
+    mbar_init(y_free, 8);
     mbar_init(done, 1);
     fence_barrier_init();
   }
-  if (warp == 17) tmem_alloc(holder, 512);
+  if (warp == 25) tmem_alloc(holder, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -227,8 +270,8 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   const uint32_t base = smem_u32(sm);
   const float* scal = reinterpret_cast<const float*>(sm + Y::kSc);
 
-  if (warp >= 16) {
-    if (warp == 16) {
+  if (warp >= 24) {
+    if (warp == 24) {
       // ---------------------------------------------------------------- keys and queries
       if (lane == 0) {
         prefetch_tmap(&c.mk);
@@ -255,7 +298,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
           mbar_wait_bounded(&kq_full[i % NST], (i / NST) & 1);
       }
       __syncwarp();
-    } else if (warp == 17) {
+    } else if (warp == 25) {
       // ---------------------------------------------------------------- products
       const uint32_t id_g = idesc_bf16_f32(128, 128);
       const uint32_t id_y = idesc_bf16_f32(128, kNV) | (1u << 16);               // B MN-major
@@ -285,18 +328,26 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         // dS: A = keys read MN-major (key columns along M; for d_k <= 64 the upper 64 rows read
         // the next tile and are not used), B = the first two parts of W V side by side; the third is added
         // to the second
-        ok = warp_wait(&kq_full[s], i / NST) && warp_wait(xw_full, i) &&
-             (i == 0 || warp_wait(ds_free, i - 1));
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t dk = sw128_mnmajor_desc(base + s * Y::kKQ, kBlk, 1024);
-          const uint64_t dx = sw128_mnmajor_desc(base + Y::kXw, kBlk, 1024);
+        ok = warp_wait(&kq_full[s], i / NST) && (i == 0 || warp_wait(ds_free, i - 1));
+#pragma unroll 1
+        for (int u = 0; u < 2 && ok; ++u) {              // 64 tokens each
+          ok = warp_wait(&xw_full[u], i);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t dk = sw128_mnmajor_desc(base + s * Y::kKQ + u * 8192, kBlk, 1024);
+            const uint64_t dx = sw128_mnmajor_desc(base + Y::kXw + u * 8192, kBlk, 1024);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            umma_bf16(tmem + kTD, dk + k * 128, dx + k * 128, id_d2, k != 0);
-            umma_bf16(tmem + kTD + kNV, dk + k * 128, dx + (2 * kBlk >> 4) + k * 128, id_d1, 1u);
+            for (int k = 0; k < 4; ++k) {
+              umma_bf16(tmem + kTD, dk + k * 128, dx + k * 128, id_d2, k != 0 || u != 0);
+              umma_bf16(tmem + kTD + kNV, dk + k * 128, dx + (2 * kBlk >> 4) + k * 128, id_d1, 1u);
+            }
+            umma_commit(&xw_free[u]);
           }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) {
           umma_commit(ds_full);
           if (!FULL) {
             umma_commit(&kq_free[s]);
@@ -341,7 +392,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       __syncwarp();
       mbar_wait_bounded(done, 0);              // before tensor memory is released
       __syncwarp();
-    } else if (warp == 18) {
+    } else if (warp == 26) {
       // ---------------------------------------------------------------- values in, y out
       if (lane == 0) {
         prefetch_tmap(&c.mv);
@@ -422,59 +473,77 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         float4* out = reinterpret_cast<float4*>(sm + Y::kSc + s * kScFloats * 4);
         out[lane] = make_float4(sf[0], sf[1], sf[2], sf[3]);
         out[32 + lane] = make_float4(dt[0], dt[1], dt[2], dt[3]);
-        if ((lane & 7) == 0) reinterpret_cast<float*>(out + 64)[lane >> 3] = sum;
+        if (lane < 24)
+          out[64 + lane] = make_float4(dt[0] * ex2(sf[0]), dt[1] * ex2(sf[1]), dt[2] * ex2(sf[2]),
+                                       dt[3] * ex2(sf[3]));
+        if ((lane & 7) == 0) reinterpret_cast<float*>(out + 88)[lane >> 3] = sum;
         warp_arrive(&sc_full[s]);
       }
     }
-  } else if (warp < 4) {
+  } else if (warp < 8) {
     // ------------------------------------------------------------------ G -> P
     if (FULL) {
-      const int t = 32 * warp + lane;
-      const uint32_t tl = tmem + (uint32_t(32 * warp) << 16);
+      const int w4 = warp & 3, t = 32 * w4 + lane, c0 = 16 * (warp >> 2);   // columns of a block
+      const uint32_t tl = tmem + (uint32_t(32 * w4) << 16);
       {
-        const uint4 z[4] = {};
+        const uint32_t z[8] = {};
 #pragma unroll 1
-        for (int j = warp + 1; j < 4; ++j) tmem_st16(tl + kTP + 16 * j, z);   // above the diagonal
+        for (int j = w4 + 1; j < 4; ++j)                 // above the diagonal
+          tmem_st8(tl + kTP + 16 * j + (c0 >> 1), z);
         tmem_st_wait();
       }
+      // s <= t within t's own block, as bits of the packed pairs
+      uint32_t keep[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        keep[e] = (c0 + 2 * e <= lane ? 0xffffu : 0u) | (c0 + 2 * e + 1 <= lane ? 0xffff0000u : 0u);
       bool ok = true;
       for (int i = 0; i < nch; ++i) {
         const int s = i % NST;
-        ok = warp_wait(&sc_full[s], i / NST) && warp_wait(g_full, i) &&
-             (i == 0 || warp_wait(y_full, i - 1));
+        ok = warp_wait(&sc_full[s], i / NST);
+        if (!ok) break;
+        const float* suf = scal + s * kScFloats;
+        const float* bs = suf + 352;
+        const float mine = suf[t];
+        ok = warp_wait(g_full, i) && (i == 0 || warp_wait(y_full, i - 1));
         if (!ok) break;
         tc_fence_after();
-        const float* suf = scal + s * kScFloats;
-        const float* dts = suf + 128;
-        const float* bs = suf + 256;
-        // log2 decay from the end of block j to t; in t's own block its negative complement, so
-        // that mid + suf[s] is the decay from s to t in every block
-        float mid = -suf[t];
-#pragma unroll 1
-        for (int jj = 0; jj < 2 * (warp + 1); ++jj) {
-          const int j = warp - (jj >> 1), col = 32 * j + 16 * (jj & 1), lim = t - col;
-          float4 l4[4], d4[4];
+        {
+          // t's own block of 32 tokens
+          const int col = 32 * w4 + c0;
+          float x[16];
+          tmem_ld16(tl + kTG + col, x);
+          const uint64_t neg = f2(-mine, -mine);
+          uint32_t p[8];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            l4[q] = *reinterpret_cast<const float4*>(suf + col + 4 * q);
-            d4[q] = *reinterpret_cast<const float4*>(dts + col + 4 * q);
+            const ulonglong2 l2 = *reinterpret_cast<const ulonglong2*>(suf + col + 4 * q);
+            const ulonglong2 d2 = *reinterpret_cast<const ulonglong2*>(suf + 128 + col + 4 * q);
+            const float2 a0 = un2(add2(l2.x, neg)), a1 = un2(add2(l2.y, neg));
+            const uint64_t w0 = mul2(f2(ex2(a0.x), ex2(a0.y)), d2.x);
+            const uint64_t w1 = mul2(f2(ex2(a1.x), ex2(a1.y)), d2.y);
+            p[2 * q] = pack2(mul2(f2(x[4 * q], x[4 * q + 1]), w0)) & keep[2 * q];
+            p[2 * q + 1] = pack2(mul2(f2(x[4 * q + 2], x[4 * q + 3]), w1)) & keep[2 * q + 1];
           }
+          tmem_st8(tl + kTP + (col >> 1), p);
+        }
+        float mid = bs[w4] - mine;           // log2 decay from the end of block j to t
+#pragma unroll 1
+        for (int j = w4 - 1; j >= 0; --j) {
+          const int col = 32 * j + c0;
+          const float rf1 = ex2(mid);
+          const uint64_t rf = f2(rf1, rf1);
+          mid += bs[j];
           float x[16];
           tmem_ld16(tl + kTG + col, x);
           uint32_t p[8];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const float lv[4] = {l4[q].x, l4[q].y, l4[q].z, l4[q].w};
-            const float dv[4] = {d4[q].x, d4[q].y, d4[q].z, d4[q].w};
-            float f[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              f[e] = 4 * q + e <= lim ? x[4 * q + e] * (ex2(mid + lv[e]) * dv[e]) : 0.f;
-            p[2 * q] = pack2(f[0], f[1]);
-            p[2 * q + 1] = pack2(f[2], f[3]);
+            const ulonglong2 c2 = *reinterpret_cast<const ulonglong2*>(suf + 256 + col + 4 * q);
+            p[2 * q] = pack2(mul2(f2(x[4 * q], x[4 * q + 1]), mul2(rf, c2.x)));
+            p[2 * q + 1] = pack2(mul2(f2(x[4 * q + 2], x[4 * q + 3]), mul2(rf, c2.y)));
           }
           tmem_st8(tl + kTP + (col >> 1), p);
-          if (jj & 1) mid += bs[j];
         }
         tmem_st_wait();
         tc_fence_before();
@@ -486,35 +555,36 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       }
       if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 62, 0);
     }
-  } else if (warp < 8) {
+  } else if (warp >= 16 && warp < 20) {
     // ------------------------------------------------------------------ W V
-    const int t = tid - 128, w4 = warp - 4;
+    const int w4 = warp & 3, t = 32 * w4 + lane;
     bool ok = true;
     for (int i = 0; i < nch; ++i) {
       const int s = i % NST, n = i / NST;
-      const int left = p1 - (p0 + i * kQ);
+      const bool live = t < p1 - (p0 + i * kQ);
       ok = warp_wait(&sc_full[s], n);
       if (!ok) break;
       const float* suf = scal + s * kScFloats;
       float after = suf[t];
-      for (int j = w4 + 1; j < 4; ++j) after += suf[256 + j];
-      const float w = suf[128 + t] * exp2f(after);
-      ok = warp_wait(&v_full[s], n) && (i == 0 || warp_wait(ds_full, i - 1));
+      for (int j = w4 + 1; j < 4; ++j) after += suf[352 + j];
+      const float w1 = suf[128 + t] * exp2f(after);
+      const uint64_t w = f2(w1, w1);
+      ok = warp_wait(&v_full[s], n) && (i == 0 || warp_wait(&xw_free[w4 >> 1], i - 1));
       if (!ok) break;
       unsigned char* vrow = sm + Y::kV + s * kBlk + t * 128;
       unsigned char* xrow = sm + Y::kXw + t * 128;
-      if (left < kQ) {
+      if (p1 - (p0 + i * kQ) < kQ) {
         // padding may hold anything, also NaN: its key and value rows are cleared
         ok = warp_wait(&kq_full[s], n);
         if (!ok) break;
-        if (t >= left) {
-          const uint4 z = make_uint4(0, 0, 0, 0);
+        if (!live) {
 #pragma unroll 1
           for (int q = 0; q < 8; ++q) {
-            reinterpret_cast<uint4*>(vrow)[q] = z;
+            reinterpret_cast<uint4*>(vrow)[q] = make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int b = 0; b < KB; ++b)
-              reinterpret_cast<uint4*>(sm + s * Y::kKQ + b * kBlk + t * 128)[q] = z;
+              reinterpret_cast<uint4*>(sm + s * Y::kKQ + b * kBlk + t * 128)[q] =
+                  make_uint4(0, 0, 0, 0);
           }
         }
       }
@@ -528,24 +598,31 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         uint32_t h1[4], h2[4], h3[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float f0 = lo_f(vw[e]) * w, f1 = hi_f(vw[e]) * w;
-          h1[e] = __byte_perm(__float_as_uint(f0), __float_as_uint(f1), 0x7632);
-          const float r0 = f0 - hi_f(__float_as_uint(f0)), r1 = f1 - hi_f(__float_as_uint(f1));
-          h2[e] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
-          const float u0 = r0 - hi_f(__float_as_uint(r0)), u1 = r1 - hi_f(__float_as_uint(r1));
-          h3[e] = __byte_perm(__float_as_uint(u0), __float_as_uint(u1), 0x7632);
+          const uint32_t sign = 0x80000000u;
+          const uint64_t f = mul2(u2(vw[e] << 16, vw[e] & 0xffff0000u), w);
+          const float2 ff = un2(f);
+          const uint32_t a0 = __float_as_uint(ff.x), a1 = __float_as_uint(ff.y);
+          h1[e] = __byte_perm(a0, a1, 0x7632);
+          const uint64_t r =
+              add2(f, u2((a0 & 0xffff0000u) ^ sign, (a1 & 0xffff0000u) ^ sign));
+          const float2 rr = un2(r);
+          const uint32_t b0 = __float_as_uint(rr.x), b1 = __float_as_uint(rr.y);
+          h2[e] = __byte_perm(b0, b1, 0x7632);
+          const float2 uu = un2(
+              add2(r, u2((b0 & 0xffff0000u) ^ sign, (b1 & 0xffff0000u) ^ sign)));
+          h3[e] = __byte_perm(__float_as_uint(uu.x), __float_as_uint(uu.y), 0x7632);
         }
         *reinterpret_cast<uint4*>(xrow + off) = make_uint4(h1[0], h1[1], h1[2], h1[3]);
         *reinterpret_cast<uint4*>(xrow + kBlk + off) = make_uint4(h2[0], h2[1], h2[2], h2[3]);
         *reinterpret_cast<uint4*>(xrow + 2 * kBlk + off) = make_uint4(h3[0], h3[1], h3[2], h3[3]);
       }
       fence_proxy_async_smem();
-      warp_arrive(xw_full);
+      warp_arrive(&xw_full[w4 >> 1]);
     }
     if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 63, 0);
-  } else if (warp < 12) {
+  } else if (warp >= 20) {
     // ------------------------------------------------------------------ state rows
-    const int k = tid - 256, w4 = warp - 8;
+    const int k = tid - 640, w4 = warp - 20;
     const uint32_t tl = tmem + (uint32_t(32 * w4) << 16);
     const bool mine = k < a.d_k, holds = k < 64 * KB;    // a key column, a row of the copy
     const float* entering = nullptr;
@@ -584,7 +661,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       const int s = i % NST;
       ok = warp_wait(&sc_full[s], i / NST);
       if (!ok) break;
-      const float4 b4 = *reinterpret_cast<const float4*>(scal + s * kScFloats + 256);
+      const float4 b4 = *reinterpret_cast<const float4*>(scal + s * kScFloats + 352);
       const float total = (b4.x + b4.y) + (b4.z + b4.w);
       warp_arrive(&sc_free[s]);
       if (!FULL) logsum += double(total);
@@ -592,8 +669,8 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       // after chunk; a fast decay would cancel in that form and is taken as it is
       const float ex = total * 0.69314718055994531f;
       const bool slow = ex > -0.5f;
-      const float mul = slow ? expm1f(ex) : expf(ex);
-      const float keep = slow ? 1.f : 0.f;
+      const float mul1 = slow ? expm1f(ex) : expf(ex), keep1 = slow ? 1.f : 0.f;
+      const uint64_t mul = f2(mul1, mul1), keep = f2(keep1, keep1);
       ok = warp_wait(ds_full, i) && (!FULL || warp_wait(s_free, i));
       if (!ok) break;
       tc_fence_after();
@@ -603,8 +680,13 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         tmem_ld8x3(tl + kTD + 8 * q, tl + kTD + kNV + 8 * q, tl + kTS + 8 * q, d);
         uint32_t x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          x[e] = __float_as_uint(fmaf(mul, d[16 + e], fmaf(keep, d[16 + e], d[e] + d[8 + e])));
+        for (int e = 0; e < 8; e += 2) {
+          const uint64_t old = f2(d[16 + e], d[17 + e]);
+          const float2 n2 = un2(fma2(
+              mul, old, fma2(keep, old, add2(f2(d[e], d[e + 1]), f2(d[8 + e], d[9 + e])))));
+          x[e] = __float_as_uint(n2.x);
+          x[e + 1] = __float_as_uint(n2.y);
+        }
         tmem_st8(tl + kTS + 8 * q, x);
         if (FULL) copy8(q, x);
       }
@@ -638,11 +720,12 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   } else {
     // ------------------------------------------------------------------ outputs
     if (FULL) {
-      const int t = tid - 384, w4 = warp - 12;
+      const int w4 = warp & 3, t = 32 * w4 + lane, hf = (warp - 8) >> 2;
       const uint32_t tl = tmem + (uint32_t(32 * w4) << 16);
       const int v0 = kNV * tile, nv = min(kNV, a.d_v - v0);
       const bool skip = a.D != nullptr;
       const float D = skip ? a.D[h] : 0.f;
+      const uint64_t D2 = f2(D, D);
       const __nv_bfloat16* zp =
           GATE ? static_cast<const __nv_bfloat16*>(a.z) + int64_t(r) * a.z_seq +
                      int64_t(h) * a.d_v + v0
@@ -658,15 +741,16 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         if (GATE && live) {
           // the row's four sectors on their way to L1 while the products run
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+          for (int q = 2 * hf; q < 2 * hf + 2; ++q)
             if (16 * q < nv) asm volatile("prefetch.global.L1 [%0];" ::"l"(zrow + 2 * q));
         }
         ok = warp_wait(&sc_full[s], i / NST);
         if (!ok) break;
         const float* suf = scal + s * kScFloats;
-        float cum = suf[256 + w4] - suf[t];
-        for (int j = 0; j < w4; ++j) cum += suf[256 + j];
+        float cum = suf[352 + w4] - suf[t];
+        for (int j = 0; j < w4; ++j) cum += suf[352 + j];
         const float ec = ex2(cum);
+        const uint64_t ec2 = f2(ec, ec);
         warp_arrive(&sc_free[s]);
         unsigned char* vrow = sm + Y::kV + s * kBlk + t * 128;
         const bool by_tma = p0 + (i + 1) * kQ <= p1 || p1 == a.P;
@@ -674,7 +758,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
-        for (int hq = 0; hq < 4; ++hq) {                 // 16 columns, two 16-byte pieces of a row
+        for (int hq = 2 * hf; hq < 2 * hf + 2; ++hq) {   // 16 columns, two 16-byte pieces of a row
           uint4 z4[2], v4[2];
           unsigned char* at[2];
 #pragma unroll
@@ -692,18 +776,22 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
             const uint32_t vw[4] = {v4[u].x, v4[u].y, v4[u].z, v4[u].w};
             const uint32_t zw[4] = {z4[u].x, z4[u].y, z4[u].z, z4[u].w};
             uint32_t ow[4];
+            uint64_t o[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int b = 8 * u + 2 * e;
-              float o0 = fmaf(ec, __uint_as_float(x2[b]), __uint_as_float(x1[b]));
-              float o1 = fmaf(ec, __uint_as_float(x2[b + 1]), __uint_as_float(x1[b + 1]));
-              o0 = fmaf(D, lo_f(vw[e]), o0);
-              o1 = fmaf(D, hi_f(vw[e]), o1);
-              if (GATE) {
-                o0 *= silu_f<__nv_bfloat16>(lo_f(zw[e]));
-                o1 *= silu_f<__nv_bfloat16>(hi_f(zw[e]));
-              }
-              ow[e] = pack2(o0, o1);
+              o[e] = fma2(ec2, u2(x2[b], x2[b + 1]), u2(x1[b], x1[b + 1]));
+            }
+            if (skip) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[e] = fma2(D2, u2(vw[e] << 16, vw[e] & 0xffff0000u), o[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (GATE)
+                o[e] = mul2(o[e], f2(silu_f<__nv_bfloat16>(lo_f(zw[e])),
+                                     silu_f<__nv_bfloat16>(hi_f(zw[e]))));
+              ow[e] = pack2(o[e]);
             }
             const uint4 o4 = make_uint4(ow[0], ow[1], ow[2], ow[3]);
             if (by_tma)
@@ -722,7 +810,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 17) {
+  if (warp == 25) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
