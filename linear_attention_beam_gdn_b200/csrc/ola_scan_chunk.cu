@@ -25,10 +25,11 @@
 //   warps 16-19  W V (thread = token s)
 //   warps 20-23  state rows (thread = key column, S^T in tensor memory): S = e^{c_C} S + dS and its
 //                bf16 copy
-//   warp 24      TMA loads of keys and queries;   warp 25  tcgen05.mma
-//   warp 26      TMA stores of y and loads of v;  warp 27  the chunk's scalars (dt, running sums)
-// Nothing but Y2 waits for the state, so the products of a chunk overlap the conversions of its
-// neighbours. A piece of a cut sequence runs twice: dS alone first (FULL = false), then, once
+//   warp 24      tcgen05.mma: dS;   warp 25  tcgen05.mma: Y1, the next chunk's G, Y2
+//   warp 26      TMA stores of y and loads of v
+//   warp 27      TMA loads of keys and queries, the chunk's scalars (dt, running sums)
+// Two issuing warps, so that neither chain (G -> P -> Y1 and W V -> dS -> S -> Y2) waits behind the
+// other's operands; nothing but Y2 waits for the state. A piece of a cut sequence runs twice: dS alone first (FULL = false), then, once
 // scan_join_kernel has made the state before every piece, the outputs.
 #include "ola_layer.cuh"
 
@@ -61,7 +62,7 @@ struct Lay {
   static constexpr uint32_t kS = kXw + 3 * kBlk;           // state copy [64 KB rows][64 columns]
   static constexpr uint32_t kSc = kS + KB * 8192;          // scalars per stage
   static constexpr uint32_t kBar = kSc + NST * kScFloats * 4;
-  static constexpr int kNBar = 6 * NST + 14;
+  static constexpr int kNBar = 7 * NST + 11;
   static constexpr uint32_t kBytes = kBar + kNBar * 8 + 16;
 };
 static_assert(Lay<1>::kBar % 8 == 0 && Lay<2>::kBar % 8 == 0, "mbarriers");
@@ -178,21 +179,6 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// Three loads of 8 columns, one wait.
-__device__ __forceinline__ void tmem_ld8x3(uint32_t ta, uint32_t tb, uint32_t tc, float (&x)[24]) {
-  uint32_t r[24];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%24];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%25];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%26];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23])
-      : "r"(ta), "r"(tb), "r"(tc)
-      : "memory");
-#pragma unroll
-  for (int j = 0; j < 24; ++j) x[j] = __uint_as_float(r[j]);
-}
-
 template <int KB, bool FULL, bool GATE>
 __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_constant__ ChunkScan c) {
   using Y = Lay<KB>;
@@ -200,24 +186,22 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   extern __shared__ __align__(1024) unsigned char sm[];
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Y::kBar);
   uint64_t* kq_full = bar;               // [NST] keys and queries landed (TMA bytes)
-  uint64_t* kq_free = bar + NST;         // [NST] ... read by the products (commit)
+  uint64_t* kq_free = bar + NST;         // [NST] ... read by the products (one commit per issuer)
   uint64_t* v_full = bar + 2 * NST;      // [NST] values landed (TMA bytes)
   uint64_t* v_done = bar + 3 * NST;      // [NST] y written over them (8 warps); dS done if !FULL
   uint64_t* sc_full = bar + 4 * NST;     // [NST] scalars written
-  uint64_t* sc_free = bar + 5 * NST;     // [NST] scalars read (commit, 4 state and 8 output warps)
-  uint64_t* one = bar + 6 * NST;
+  uint64_t* sc_free = bar + 5 * NST;     // [NST] scalars read (commits, state and output warps)
+  uint64_t* x_done = bar + 6 * NST;      // [NST] values read by the W V warps (4 warps)
+  uint64_t* one = bar + 7 * NST;
   uint64_t* xw_full = one + 0;           // [2] W V of 64 tokens written (2 warps)
   uint64_t* xw_free = one + 2;           // [2] ... read by dS (commit)
   uint64_t* ds_full = one + 4;           // dS done
-  uint64_t* ds_free = one + 5;           // dS read (4 warps)
-  uint64_t* g_full = one + 6;            // G done
-  uint64_t* g_free = one + 7;            // G read (8 warps)
-  uint64_t* p_full = one + 8;            // P written (8 warps)
-  uint64_t* s_full = one + 9;            // state copy written (4 warps)
-  uint64_t* s_free = one + 10;           // Y2 done: state copy read
-  uint64_t* y_full = one + 11;           // Y1 and Y2 done (and P read)
-  uint64_t* y_free = one + 12;           // Y1 and Y2 read (8 warps)
-  uint64_t* done = one + 13;             // every MMA completed
+  uint64_t* g_full = one + 5;            // G done, and Y1 of the chunk before
+  uint64_t* p_full = one + 6;            // G read and P written (8 warps)
+  uint64_t* s_full = one + 7;            // dS read, state and its copy written (4 warps)
+  uint64_t* y_full = one + 8;            // Y1 and Y2 done
+  uint64_t* y_free = one + 9;            // Y1 and Y2 read (8 warps)
+  uint64_t* done = one + 10;             // every MMA completed (both issuers)
   uint32_t* holder = reinterpret_cast<uint32_t*>(bar + Y::kNBar);
   const ScanArgs& a = c.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -240,26 +224,24 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   if (tid == 0) {
     for (int s = 0; s < NST; ++s) {
       mbar_init(&kq_full[s], 1);
-      mbar_init(&kq_free[s], 1);
+      mbar_init(&kq_free[s], FULL ? 2 : 1);
       mbar_init(&v_full[s], 1);
       mbar_init(&v_done[s], FULL ? 8 : 1);
       mbar_init(&sc_full[s], 1);
-      mbar_init(&sc_free[s], FULL ? 13 : 5);
+      mbar_init(&sc_free[s], FULL ? 14 : 5);
+      mbar_init(&x_done[s], 4);
     }
     for (int u = 0; u < 2; ++u) {
       mbar_init(&xw_full[u], 2);
       mbar_init(&xw_free[u], 1);
     }
     mbar_init(ds_full, 1);
-    mbar_init(ds_free, 4);
     mbar_init(g_full, 1);
-    mbar_init(g_free, 8);
     mbar_init(p_full, 8);
     mbar_init(s_full, 4);
-    mbar_init(s_free, 1);
     mbar_init(y_full, 1);
     mbar_init(y_free, 8);
-    mbar_init(done, 1);
+    mbar_init(done, 2);
     fence_barrier_init();
   }
   if (warp == 25) tmem_alloc(holder, 512);
@@ -272,63 +254,16 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
 
   if (warp >= 24) {
     if (warp == 24) {
-      // ---------------------------------------------------------------- keys and queries
-      if (lane == 0) {
-        prefetch_tmap(&c.mk);
-        if (FULL) prefetch_tmap(&c.mq);
-        int issued = 0;
-        for (int i = 0; i < nch; ++i) {
-          const int s = i % NST, n = i / NST;
-          if (n > 0 && !mbar_wait_bounded(&kq_free[s], (n - 1) & 1)) {
-            report_error(a.err, OLA_ERR_TIMEOUT, 60, i);
-            break;
-          }
-          mbar_arrive_expect_tx(&kq_full[s], (FULL ? 2 : 1) * KB * kBlk);
-          unsigned char* st = sm + s * Y::kKQ;
-          const int p = p0 + i * kQ;
-#pragma unroll
-          for (int b = 0; b < KB; ++b) {
-            tma_load_4d(st + b * kBlk, &c.mk, &kq_full[s], 64 * b, g, p, r);
-            if (FULL) tma_load_4d(st + Y::kQr + b * kBlk, &c.mq, &kq_full[s], 64 * b, g, p, r);
-          }
-          issued = i + 1;
-        }
-        // the copies still in flight land before the block exits
-        for (int i = issued > NST ? issued - NST : 0; i < issued; ++i)
-          mbar_wait_bounded(&kq_full[i % NST], (i / NST) & 1);
-      }
-      __syncwarp();
-    } else if (warp == 25) {
-      // ---------------------------------------------------------------- products
-      const uint32_t id_g = idesc_bf16_f32(128, 128);
-      const uint32_t id_y = idesc_bf16_f32(128, kNV) | (1u << 16);               // B MN-major
+      // ---------------------------------------------------------------- product dS
+      // A = keys read MN-major (key columns along M; for d_k <= 64 the upper 64 rows read the next
+      // tile and are not used), B = the first two parts of W V side by side; the third is added to
+      // the second
       const uint32_t id_d2 = idesc_bf16_f32_amn(128, 2 * kNV) | (1u << 16);      // A, B MN-major
       const uint32_t id_d1 = idesc_bf16_f32_amn(128, kNV) | (1u << 16);
-      auto issue_g = [&](int i) -> bool {
+      bool ok = true;
+      for (int i = 0; i < nch; ++i) {
         const int s = i % NST;
-        if (!warp_wait(&kq_full[s], i / NST) || (i > 0 && !warp_wait(g_free, i - 1)))
-          return false;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t dk = sw128_kmajor_desc(base + s * Y::kKQ);
-          const uint64_t dq = sw128_kmajor_desc(base + s * Y::kKQ + Y::kQr);
-#pragma unroll
-          for (int k = 0; k < 4 * KB; ++k) {
-            const uint64_t off = (k >> 2) * (kBlk >> 4) + (k & 3) * 2;
-            umma_bf16(tmem + kTG, dq + off, dk + off, id_g, k != 0);
-          }
-          umma_commit(g_full);
-        }
-        __syncwarp();
-        return true;
-      };
-      bool ok = !FULL || nch == 0 || issue_g(0);
-      for (int i = 0; i < nch && ok; ++i) {
-        const int s = i % NST;
-        // dS: A = keys read MN-major (key columns along M; for d_k <= 64 the upper 64 rows read
-        // the next tile and are not used), B = the first two parts of W V side by side; the third is added
-        // to the second
-        ok = warp_wait(&kq_full[s], i / NST) && (i == 0 || warp_wait(ds_free, i - 1));
+        ok = warp_wait(&kq_full[s], i / NST) && warp_wait(s_full, i);
 #pragma unroll 1
         for (int u = 0; u < 2 && ok; ++u) {              // 64 tokens each
           ok = warp_wait(&xw_full[u], i);
@@ -343,54 +278,87 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
               umma_bf16(tmem + kTD + kNV, dk + k * 128, dx + (2 * kBlk >> 4) + k * 128, id_d1, 1u);
             }
             umma_commit(&xw_free[u]);
+            if (u == 1) {
+              umma_commit(ds_full);
+              umma_commit(&kq_free[s]);
+              umma_commit(&sc_free[s]);
+              if (!FULL) umma_commit(&v_done[s]);
+            }
           }
           __syncwarp();
         }
         if (!ok) break;
-        if (elect_one()) {
-          umma_commit(ds_full);
-          if (!FULL) {
-            umma_commit(&kq_free[s]);
-            umma_commit(&v_done[s]);
-            umma_commit(&sc_free[s]);
-          }
-        }
-        __syncwarp();
-        if (!FULL) continue;
-        // Y2: A = queries, B = the state copy (rows = key columns)
-        ok = warp_wait(s_full, i) && (i == 0 || warp_wait(y_free, i - 1));
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t dq = sw128_kmajor_desc(base + s * Y::kKQ + Y::kQr);
-          const uint64_t dsd = sw128_mnmajor_desc(base + Y::kS, kBlk, 1024);
-#pragma unroll
-          for (int k = 0; k < 4 * KB; ++k)
-            umma_bf16(tmem + kTY2, dq + (k >> 2) * (kBlk >> 4) + (k & 3) * 2, dsd + k * 128, id_y,
-                      k != 0);
-          umma_commit(s_free);
-          umma_commit(&kq_free[s]);
-        }
-        __syncwarp();
-        if (i + 1 < nch && !(ok = issue_g(i + 1))) break;
-        // Y1: A = P in tensor memory, B = the values (rows = tokens)
-        ok = warp_wait(&v_full[s], i / NST) && warp_wait(p_full, i);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t dv = sw128_mnmajor_desc(base + Y::kV + s * kBlk, kBlk, 1024);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            umma_bf16_ts(tmem + kTY1, tmem + kTP + k * 8, dv + k * 128, id_y, k != 0);
-          umma_commit(y_full);
-          umma_commit(&sc_free[s]);
-        }
-        __syncwarp();
       }
-      if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 61, 0);
+      if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 60, 0);
       if (elect_one()) umma_commit(done);
       __syncwarp();
-      mbar_wait_bounded(done, 0);              // before tensor memory is released
+    } else if (warp == 25) {
+      // ---------------------------------------------------------------- products Y1, G, Y2
+      if (FULL) {
+        const uint32_t id_g = idesc_bf16_f32(128, 128);
+        const uint32_t id_y = idesc_bf16_f32(128, kNV) | (1u << 16);             // B MN-major
+        bool ok = true;
+#pragma unroll 1
+        for (int i = -1; i < nch && ok; ++i) {
+          const int s = i < 0 ? 0 : i % NST;
+          if (i >= 0) {
+            // Y1: A = P in tensor memory, B = the values (rows = tokens)
+            ok = warp_wait(p_full, i) && warp_wait(&v_full[s], i / NST) &&
+                 (i == 0 || warp_wait(y_free, i - 1));
+            // (the values' rows behind the end of a padded sequence are cleared by then)
+            if (ok && p1 - (p0 + i * kQ) < kQ) ok = warp_wait(&x_done[s], i / NST);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t dv = sw128_mnmajor_desc(base + Y::kV + s * kBlk, kBlk, 1024);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                umma_bf16_ts(tmem + kTY1, tmem + kTP + k * 8, dv + k * 128, id_y, k != 0);
+            }
+            __syncwarp();
+          }
+          if (i + 1 < nch) {
+            // G of the next chunk: queries x keys
+            const int s1 = (i + 1) % NST;
+            ok = warp_wait(&kq_full[s1], (i + 1) / NST);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t dk = sw128_kmajor_desc(base + s1 * Y::kKQ);
+              const uint64_t dq = sw128_kmajor_desc(base + s1 * Y::kKQ + Y::kQr);
+#pragma unroll
+              for (int k = 0; k < 4 * KB; ++k) {
+                const uint64_t off = (k >> 2) * (kBlk >> 4) + (k & 3) * 2;
+                umma_bf16(tmem + kTG, dq + off, dk + off, id_g, k != 0);
+              }
+              umma_commit(g_full);
+            }
+            __syncwarp();
+          }
+          if (i >= 0) {
+            // Y2: A = queries, B = the state copy (rows = key columns)
+            ok = warp_wait(s_full, i);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t dq = sw128_kmajor_desc(base + s * Y::kKQ + Y::kQr);
+              const uint64_t dsd = sw128_mnmajor_desc(base + Y::kS, kBlk, 1024);
+#pragma unroll
+              for (int k = 0; k < 4 * KB; ++k)
+                umma_bf16(tmem + kTY2, dq + (k >> 2) * (kBlk >> 4) + (k & 3) * 2, dsd + k * 128,
+                          id_y, k != 0);
+              umma_commit(y_full);
+              umma_commit(&kq_free[s]);
+              umma_commit(&sc_free[s]);
+            }
+            __syncwarp();
+          }
+        }
+        if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 61, 0);
+      }
+      if (elect_one()) umma_commit(done);
+      __syncwarp();
+      mbar_wait_bounded(done, 0);              // both issuers, before tensor memory is released
       __syncwarp();
     } else if (warp == 26) {
       // ---------------------------------------------------------------- values in, y out
@@ -424,7 +392,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       }
       __syncwarp();
     } else {
-      // ---------------------------------------------------------------- scalars
+      // ---------------------------------------------------------------- keys, queries, scalars
       // lane = 4 tokens, 8 lanes = a block of 32; every sum runs over tokens behind the token
       const float A2 = a.A[h] * 1.4426950408889634f;
       const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
@@ -438,8 +406,29 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         }
       };
       load_dt(0);
+      if (lane == 0) {
+        prefetch_tmap(&c.mk);
+        if (FULL) prefetch_tmap(&c.mq);
+      }
+      int issued = 0;
       for (int i = 0; i < nch; ++i) {
         const int s = i % NST, n = i / NST;
+        if (n > 0 && !warp_wait(&kq_free[s], n - 1)) {
+          if (lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 68, i);
+          break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&kq_full[s], (FULL ? 2 : 1) * KB * kBlk);
+          unsigned char* st = sm + s * Y::kKQ;
+          const int p = p0 + i * kQ;
+#pragma unroll
+          for (int b = 0; b < KB; ++b) {
+            tma_load_4d(st + b * kBlk, &c.mk, &kq_full[s], 64 * b, g, p, r);
+            if (FULL) tma_load_4d(st + Y::kQr + b * kBlk, &c.mq, &kq_full[s], 64 * b, g, p, r);
+          }
+        }
+        __syncwarp();
+        issued = i + 1;
         const int left = p1 - (p0 + i * kQ);            // tokens of the piece from here on
         float dt[4], sf[4];
 #pragma unroll
@@ -479,6 +468,10 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         if ((lane & 7) == 0) reinterpret_cast<float*>(out + 88)[lane >> 3] = sum;
         warp_arrive(&sc_full[s]);
       }
+      // the copies still in flight land before the block exits
+      for (int i = issued > NST ? issued - NST : 0; i < issued; ++i)
+        mbar_wait_bounded(&kq_full[i % NST], (i / NST) & 1);
+      __syncwarp();
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------------ G -> P
@@ -505,7 +498,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         const float* suf = scal + s * kScFloats;
         const float* bs = suf + 352;
         const float mine = suf[t];
-        ok = warp_wait(g_full, i) && (i == 0 || warp_wait(y_full, i - 1));
+        ok = warp_wait(g_full, i);
         if (!ok) break;
         tc_fence_after();
         {
@@ -547,11 +540,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         }
         tmem_st_wait();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(g_free);
-          mbar_arrive(p_full);
-        }
+        warp_arrive(p_full);
       }
       if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 62, 0);
     }
@@ -590,7 +579,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       }
       // a product of 24 bits is its upper 8 bits, the next 8 and the rest, each cut off exactly
       uint4 nx = *reinterpret_cast<const uint4*>(vrow + ((t & 7) << 4));
-#pragma unroll 1
+#pragma unroll 2
       for (int q = 0; q < 8; ++q) {
         const uint32_t off = uint32_t((q ^ (t & 7)) << 4);
         const uint32_t vw[4] = {nx.x, nx.y, nx.z, nx.w};
@@ -617,7 +606,11 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         *reinterpret_cast<uint4*>(xrow + 2 * kBlk + off) = make_uint4(h3[0], h3[1], h3[2], h3[3]);
       }
       fence_proxy_async_smem();
-      warp_arrive(&xw_full[w4 >> 1]);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&xw_full[w4 >> 1]);
+        mbar_arrive(&x_done[s]);
+      }
     }
     if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 63, 0);
   } else if (warp >= 20) {
@@ -651,10 +644,9 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       if (FULL) copy8(q, x);
     }
     tmem_st_wait();
-    if (FULL) {
-      fence_proxy_async_smem();
-      warp_arrive(s_full);
-    }
+    tc_fence_before();
+    if (FULL) fence_proxy_async_smem();
+    warp_arrive(s_full);
     double logsum = 0.0;
     bool ok = true;
     for (int i = 0; i < nch; ++i) {
@@ -671,33 +663,33 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       const bool slow = ex > -0.5f;
       const float mul1 = slow ? expm1f(ex) : expf(ex), keep1 = slow ? 1.f : 0.f;
       const uint64_t mul = f2(mul1, mul1), keep = f2(keep1, keep1);
-      ok = warp_wait(ds_full, i) && (!FULL || warp_wait(s_free, i));
+      ok = warp_wait(ds_full, i) && (!FULL || warp_wait(y_full, i));
       if (!ok) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int q = 0; q < 8; ++q) {
-        float d[24];
-        tmem_ld8x3(tl + kTD + 8 * q, tl + kTD + kNV + 8 * q, tl + kTS + 8 * q, d);
-        uint32_t x[8];
+      for (int q = 0; q < 8; q += 2) {
+        float d[48];
+        tmem_ld16x3(tl + kTD + 8 * q, tl + kTD + kNV + 8 * q, tl + kTS + 8 * q, d);
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const uint64_t old = f2(d[16 + e], d[17 + e]);
-          const float2 n2 = un2(fma2(
-              mul, old, fma2(keep, old, add2(f2(d[e], d[e + 1]), f2(d[8 + e], d[9 + e])))));
-          x[e] = __float_as_uint(n2.x);
-          x[e + 1] = __float_as_uint(n2.y);
+        for (int u = 0; u < 2; ++u) {
+          uint32_t x[8];
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const int b = 8 * u + e;
+            const uint64_t old = f2(d[32 + b], d[33 + b]);
+            const float2 n2 = un2(fma2(
+                mul, old, fma2(keep, old, add2(f2(d[b], d[b + 1]), f2(d[16 + b], d[17 + b])))));
+            x[e] = __float_as_uint(n2.x);
+            x[e + 1] = __float_as_uint(n2.y);
+          }
+          tmem_st8(tl + kTS + 8 * (q + u), x);
+          if (FULL) copy8(q + u, x);
         }
-        tmem_st8(tl + kTS + 8 * q, x);
-        if (FULL) copy8(q, x);
       }
       tmem_st_wait();
       tc_fence_before();
       if (FULL) fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(ds_free);
-        if (FULL) mbar_arrive(s_full);
-      }
+      warp_arrive(s_full);
     }
     if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 64, 0);
     float* out = nullptr;
@@ -754,7 +746,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         warp_arrive(&sc_free[s]);
         unsigned char* vrow = sm + Y::kV + s * kBlk + t * 128;
         const bool by_tma = p0 + (i + 1) * kQ <= p1 || p1 == a.P;
-        ok = warp_wait(y_full, i);
+        ok = warp_wait(y_full, i) && warp_wait(&x_done[s], i / NST);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
