@@ -19,7 +19,7 @@
 //
 // One block per (sequence, head, 64 value columns, piece), one per SM:
 //   warps 0-7    G -> P (thread = token t, half of the columns; P into tensor memory as the A
-//                operand of Y1)
+//                operand of Y1); warps 0-3 also the next chunk's scalars (dt, running sums)
 //   warps 8-15   outputs (thread = token t, half of the columns): Y1 + e^{c_t} Y2, D, gate; y staged
 //                over v
 //   warps 16-19  W V (thread = token s)
@@ -27,7 +27,7 @@
 //                bf16 copy
 //   warp 24      tcgen05.mma: dS;   warp 25  tcgen05.mma: Y1, the next chunk's G, Y2
 //   warp 26      TMA stores of y and loads of v
-//   warp 27      TMA loads of keys and queries, the chunk's scalars (dt, running sums)
+//   warp 27      TMA loads of keys and queries
 // Two issuing warps, so that neither chain (G -> P -> Y1 and W V -> dS -> S -> Y2) waits behind the
 // other's operands; nothing but Y2 waits for the state. A piece of a cut sequence runs twice: dS alone first (FULL = false), then, once
 // scan_join_kernel has made the state before every piece, the outputs.
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   uint64_t* kq_free = bar + NST;         // [NST] ... read by the products (one commit per issuer)
   uint64_t* v_full = bar + 2 * NST;      // [NST] values landed (TMA bytes)
   uint64_t* v_done = bar + 3 * NST;      // [NST] y written over them (8 warps); dS done if !FULL
-  uint64_t* sc_full = bar + 4 * NST;     // [NST] scalars written
+  uint64_t* sc_full = bar + 4 * NST;     // [NST] scalars written (4 warps)
   uint64_t* sc_free = bar + 5 * NST;     // [NST] scalars read (commits, state and output warps)
   uint64_t* x_done = bar + 6 * NST;      // [NST] values read by the W V warps (4 warps)
   uint64_t* one = bar + 7 * NST;
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       mbar_init(&kq_free[s], FULL ? 2 : 1);
       mbar_init(&v_full[s], 1);
       mbar_init(&v_done[s], FULL ? 8 : 1);
-      mbar_init(&sc_full[s], 1);
+      mbar_init(&sc_full[s], 4);
       mbar_init(&sc_free[s], FULL ? 14 : 5);
       mbar_init(&x_done[s], 4);
     }
@@ -392,32 +392,17 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       }
       __syncwarp();
     } else {
-      // ---------------------------------------------------------------- keys, queries, scalars
-      // lane = 4 tokens, 8 lanes = a block of 32; every sum runs over tokens behind the token
-      const float A2 = a.A[h] * 1.4426950408889634f;
-      const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
-      const float* dtp = a.dt + int64_t(r) * a.P * a.H + h;
-      float raw[4];
-      auto load_dt = [&](int i) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int p = p0 + i * kQ + 4 * lane + e;
-          raw[e] = i < nch && p < p1 ? __ldg(dtp + int64_t(p) * a.H) : 0.f;
-        }
-      };
-      load_dt(0);
+      // ---------------------------------------------------------------- keys, queries
       if (lane == 0) {
         prefetch_tmap(&c.mk);
         if (FULL) prefetch_tmap(&c.mq);
-      }
-      int issued = 0;
-      for (int i = 0; i < nch; ++i) {
-        const int s = i % NST, n = i / NST;
-        if (n > 0 && !warp_wait(&kq_free[s], n - 1)) {
-          if (lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 68, i);
-          break;
-        }
-        if (lane == 0) {
+        int issued = 0;
+        for (int i = 0; i < nch; ++i) {
+          const int s = i % NST, n = i / NST;
+          if (n > 0 && !mbar_wait_bounded(&kq_free[s], (n - 1) & 1)) {
+            report_error(a.err, OLA_ERR_TIMEOUT, 68, i);
+            break;
+          }
           mbar_arrive_expect_tx(&kq_full[s], (FULL ? 2 : 1) * KB * kBlk);
           unsigned char* st = sm + s * Y::kKQ;
           const int p = p0 + i * kQ;
@@ -426,58 +411,58 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
             tma_load_4d(st + b * kBlk, &c.mk, &kq_full[s], 64 * b, g, p, r);
             if (FULL) tma_load_4d(st + Y::kQr + b * kBlk, &c.mq, &kq_full[s], 64 * b, g, p, r);
           }
+          issued = i + 1;
         }
-        __syncwarp();
-        issued = i + 1;
-        const int left = p1 - (p0 + i * kQ);            // tokens of the piece from here on
-        float dt[4], sf[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // tokens behind the end take no part: dt = 0
-          dt[e] = raw[e] + bias;
-          if (a.softplus) dt[e] = softplus_f(dt[e]);
-          if (4 * lane + e >= left) dt[e] = 0.f;
-        }
-        load_dt(i + 1);
-        // a decay below 2^-256 is 0; the clamp keeps sums of resets finite
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 3; e >= 0; --e) {
-          sf[e] = sum;
-          sum += fmaxf(dt[e] * A2, -256.f);
-        }
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) {
-          const float d = __shfl_down_sync(kFull, sum, o);
-          if ((lane & 7) + o < 8) sum += d;
-        }
-        float behind = __shfl_down_sync(kFull, sum, 1);
-        if ((lane & 7) == 7) behind = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sf[e] += behind;
-        if (n > 0 && !warp_wait(&sc_free[s], n - 1)) {
-          if (lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 67, i);
-          break;
-        }
-        float4* out = reinterpret_cast<float4*>(sm + Y::kSc + s * kScFloats * 4);
-        out[lane] = make_float4(sf[0], sf[1], sf[2], sf[3]);
-        out[32 + lane] = make_float4(dt[0], dt[1], dt[2], dt[3]);
-        if (lane < 24)
-          out[64 + lane] = make_float4(dt[0] * ex2(sf[0]), dt[1] * ex2(sf[1]), dt[2] * ex2(sf[2]),
-                                       dt[3] * ex2(sf[3]));
-        if ((lane & 7) == 0) reinterpret_cast<float*>(out + 88)[lane >> 3] = sum;
-        warp_arrive(&sc_full[s]);
+        // the copies still in flight land before the block exits
+        for (int i = issued > NST ? issued - NST : 0; i < issued; ++i)
+          mbar_wait_bounded(&kq_full[i % NST], (i / NST) & 1);
       }
-      // the copies still in flight land before the block exits
-      for (int i = issued > NST ? issued - NST : 0; i < issued; ++i)
-        mbar_wait_bounded(&kq_full[i % NST], (i / NST) & 1);
       __syncwarp();
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------------ G -> P
-    if (FULL) {
-      const int w4 = warp & 3, t = 32 * w4 + lane, c0 = 16 * (warp >> 2);   // columns of a block
-      const uint32_t tl = tmem + (uint32_t(32 * w4) << 16);
+    const int w4 = warp & 3, t = 32 * w4 + lane, c0 = 16 * (warp >> 2);   // columns of a block
+    const uint32_t tl = tmem + (uint32_t(32 * w4) << 16);
+    // the scalars of chunk i (thread = token): every sum runs over the tokens behind the token, in
+    // its block of 32
+    const float A2 = a.A[h] * 1.4426950408889634f;
+    const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+    const float* dtp = a.dt + int64_t(r) * a.P * a.H + h;
+    auto load_dt = [&](int i) -> float {
+      const int p = p0 + i * kQ + t;
+      return i < nch && p < p1 ? __ldg(dtp + int64_t(p) * a.H) : 0.f;
+    };
+    float raw = c0 == 0 ? load_dt(0) : 0.f;
+    auto scalars = [&](int i) -> bool {
+      const int s = i % NST, n = i / NST;
+      // tokens behind the end take no part: dt = 0
+      float dt = raw + bias;
+      if (a.softplus) dt = softplus_f(dt);
+      if (t >= p1 - (p0 + i * kQ)) dt = 0.f;
+      raw = load_dt(i + 1);
+      // a decay below 2^-256 is 0; the clamp keeps sums of resets finite
+      float sum = fmaxf(dt * A2, -256.f);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float d = __shfl_down_sync(kFull, sum, o);
+        if (lane + o < 32) sum += d;
+      }
+      float suf = __shfl_down_sync(kFull, sum, 1);
+      if (lane == 31) suf = 0.f;
+      if (n > 0 && !warp_wait(&sc_free[s], n - 1)) return false;
+      float* out = reinterpret_cast<float*>(sm + Y::kSc) + s * kScFloats;
+      out[t] = suf;
+      out[128 + t] = dt;
+      if (w4 < 3) out[256 + t] = dt * ex2(suf);
+      if (lane == 0) out[352 + w4] = sum;
+      warp_arrive(&sc_full[s]);
+      return true;
+    };
+    bool ok = c0 != 0 || nch == 0 || scalars(0);
+    if (!FULL) {
+      for (int i = 1; i < nch && ok && c0 == 0; ++i) ok = scalars(i);
+      if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 67, 0);
+    } else {
       {
         const uint32_t z[8] = {};
 #pragma unroll 1
@@ -490,8 +475,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         keep[e] = (c0 + 2 * e <= lane ? 0xffffu : 0u) | (c0 + 2 * e + 1 <= lane ? 0xffff0000u : 0u);
-      bool ok = true;
-      for (int i = 0; i < nch; ++i) {
+      for (int i = 0; i < nch && ok; ++i) {
         const int s = i % NST;
         ok = warp_wait(&sc_full[s], i / NST);
         if (!ok) break;
@@ -541,6 +525,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         tmem_st_wait();
         tc_fence_before();
         warp_arrive(p_full);
+        if (c0 == 0 && i + 1 < nch) ok = scalars(i + 1);
       }
       if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 62, 0);
     }
