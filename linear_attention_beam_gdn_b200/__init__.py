@@ -442,80 +442,108 @@ class Decoder:
 #
 # Each call runs on the device of its first tensor and on `stream` (default: that device's current
 # stream), allocates only the outputs and scratch that it is not given (they belong to that
-# stream), and does not wait. Inputs
-# that may be strided are [sequence, token, ...] with contiguous channels, so a slice of a wide
-# projection's columns is taken as it is.
-
-def _on(x, name, shape, dtype, device, strided=False):
-    """Checks a tensor argument of an operator; returns its pointer."""
-    if not strided:
-        return _need(x, shape, dtype, name, device)
-    torch = _torch()
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if x.device != device:
-        raise ValueError(f"{name} is on {x.device}, expected {device}")
-    if tuple(x.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
-    if x.dtype != dtype:
-        raise TypeError(f"{name} has dtype {x.dtype}, expected {dtype}")
-    width, inner = 1, True
-    for n, s in zip(reversed(x.shape[2:]), reversed(x.stride()[2:])):
-        inner = inner and (n == 1 or s == width)
-        width *= n
-    R, P = x.shape[:2]
-    if not inner or (P > 1 and x.stride(1) < width) or (R > 1 and x.stride(0) < 1):
-        raise ValueError(f"{name}: channels must be contiguous and tokens must not overlap")
-    return x.data_ptr()
-
-
-def _strides(x):
-    """(token, sequence) strides in elements; 0 (contiguous) where the extent is 1."""
-    return (x.stride(1) if x.shape[1] > 1 else 0), (x.stride(0) if x.shape[0] > 1 else 0)
-
-
-def _tok_strides(x):
-    """The same, with the token stride of a single token made explicit."""
-    tok, seq = _strides(x)
-    width = 1
-    for n in x.shape[2:]:
-        width *= n
-    return tok or width, seq or max(1, x.shape[1]) * (tok or width)
-
-
-def _first(x, name, ndim):
-    torch = _torch()
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if x.device.type != "cuda":
-        raise ValueError(f"{name} must be on a CUDA device")
-    if x.dim() != ndim:
-        raise ValueError(f"{name} has {x.dim()} dimensions, expected {ndim}")
-    _dtype_code(x.dtype)
-    return x.device
-
+# stream), and does not wait. Inputs that may be strided are [sequence, token, ...] with contiguous
+# channels, so a slice of a wide projection's columns is taken as it is. A decode step of a few
+# tokens costs less on the device than its argument checks can on the host, so these are kept to a
+# few attribute reads per tensor.
 
 class _Scope:
     """The device of a call and the stream its kernels and allocations belong to."""
 
-    def __init__(self, device, stream):
+    def __init__(self, index, stream):
         torch = _torch()
-        self.device = torch.cuda.device(device)
-        self.stream = torch.cuda.stream(stream) if stream is not None else None
+        self.index = index
+        self.device = self.stream = None
+        if torch._C._cuda_getDevice() != index:
+            self.device = torch.cuda.device(index)
+        if stream is not None:
+            self.stream = torch.cuda.stream(stream)
+        self.raw = stream.cuda_stream if stream is not None else None
 
     def __enter__(self):
-        self.device.__enter__()
+        if self.device is not None:
+            self.device.__enter__()
         if self.stream is not None:
             self.stream.__enter__()
+        else:
+            self.raw = _torch()._C._cuda_getCurrentRawStream(self.index)
+        return self.raw
 
     def __exit__(self, *exc):
         if self.stream is not None:
             self.stream.__exit__(*exc)
-        self.device.__exit__(*exc)
+        if self.device is not None:
+            self.device.__exit__(*exc)
 
 
-def _opt(x, name, shape, dtype, device, strided=False):
-    return None if x is None else _on(x, name, shape, dtype, device, strided)
+def _first(x, name, ndim):
+    """Checks the leading tensor of a call; returns (device index, dtype code)."""
+    torch = _torch()
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    index = x.get_device()
+    if index < 0 or not x.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if x.dim() != ndim:
+        raise ValueError(f"{name} has {x.dim()} dimensions, expected {ndim}")
+    return index, _dtype_code(x.dtype)
+
+
+def _bad(x, name, shape, dtype, index):
+    """Raises what is wrong with a tensor argument."""
+    torch = _torch()
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.get_device() != index or not x.is_cuda:
+        raise ValueError(f"{name} is on {x.device}, expected cuda:{index}")
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
+    if x.dtype != dtype:
+        raise TypeError(f"{name} has dtype {x.dtype}, expected {dtype}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _ptr(x, name, shape, dtype, index):
+    """Pointer of a contiguous tensor argument."""
+    try:
+        if (x.shape == shape and x.dtype == dtype and x.is_cuda and x.get_device() == index and
+                x.is_contiguous()):
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    _bad(x, name, shape, dtype, index)
+
+
+def _opt(x, name, shape, dtype, index):
+    return None if x is None else _ptr(x, name, shape, dtype, index)
+
+
+def _rows(x, name, shape, dtype, index):
+    """(pointer, token stride, sequence stride) of a [sequence, token, ...] argument whose channels
+    are contiguous; strides of 0 stand for a contiguous tensor."""
+    try:
+        fine = x.shape == shape and x.dtype == dtype and x.is_cuda and x.get_device() == index
+    except AttributeError:
+        fine = False
+    if not fine:
+        _bad(x, name, shape, dtype, index)
+    if x.is_contiguous():
+        return x.data_ptr(), 0, 0
+    st, width = x.stride(), 1
+    for n, s in zip(reversed(shape[2:]), reversed(st[2:])):
+        if n != 1 and s != width:
+            raise ValueError(f"{name}: channels must be contiguous")
+        width *= n
+    R, P = shape[:2]
+    tok = st[1] if P > 1 else width
+    seq = st[0] if R > 1 else P * tok
+    if tok < width or seq < 1:
+        raise ValueError(f"{name}: tokens must not overlap")
+    return x.data_ptr(), tok, seq
+
+
+def _opt_rows(x, name, shape, dtype, index):
+    return (None, 0, 0) if x is None else _rows(x, name, shape, dtype, index)
 
 
 def layer_status(device=None, stream=None) -> int:
@@ -529,6 +557,12 @@ def layer_status(device=None, stream=None) -> int:
     return st
 
 
+def _taps(w):
+    if not isinstance(w, _torch().Tensor) or w.dim() != 2:
+        raise ValueError("w must be a tensor [C, W]")
+    return max(w.shape[1], 1)
+
+
 def conv(x, w, bias=None, *, state=None, lens=None, silu=True, out=None, state_out=None,
          stream=None):
     """Short causal convolution of a prompt (ola_conv): x [R, P, C] (bf16 or fp32, may be a column
@@ -536,26 +570,22 @@ def conv(x, w, bias=None, *, state=None, lens=None, silu=True, out=None, state_o
     [R] int32 for a padded batch. Returns (y [R, P, C], state_out [R, W-1, C]); rows of `out`
     behind a sequence's end are not written. state_out may be `state`."""
     torch = _torch()
-    dev = _first(x, "x", 3)
-    R, P, C = x.shape
-    if w.dim() != 2:
-        raise ValueError("w must be [C, W]")
-    W = w.shape[1]
-    dt = x.dtype
-    with _Scope(dev, stream):
+    ix, code = _first(x, "x", 3)
+    R, P, C = shape = x.shape
+    W, dt, f32 = _taps(w), x.dtype, torch.float32
+    with _Scope(ix, stream) as st:
         if out is None:
-            out = torch.empty((R, P, C), device=dev, dtype=dt)
+            out = torch.empty(shape, device=x.device, dtype=dt)
+        win = (R, W - 1, C)
         if state_out is None:
-            state_out = torch.empty((R, max(W - 1, 0), C), device=dev, dtype=dt)
-        args = [_on(x, "x", (R, P, C), dt, dev, True), _on(w, "w", (C, W), torch.float32, dev),
-                _opt(bias, "bias", (C,), torch.float32, dev),
-                _opt(state, "state", (R, W - 1, C), dt, dev),
-                _opt(lens, "lens", (R,), torch.int32, dev),
-                _on(out, "out", (R, P, C), dt, dev, True),
-                _on(state_out, "state_out", (R, W - 1, C), dt, dev)]
-        d = ConvDesc(R, P, C, W, _dtype_code(dt), int(bool(silu)), *_tok_strides(x),
-                     *_tok_strides(out))
-        _check(ola_conv(d, *args, _stream_ptr(stream)), "ola_conv")
+            state_out = torch.empty(win, device=x.device, dtype=dt)
+        xp, x_tok, x_seq = _rows(x, "x", shape, dt, ix)
+        yp, y_tok, y_seq = _rows(out, "out", shape, dt, ix)
+        d = ConvDesc(R, P, C, W, code, bool(silu), x_tok, x_seq, y_tok, y_seq)
+        _check(ola_conv(d, xp, _ptr(w, "w", (C, W), f32, ix), _opt(bias, "bias", (C,), f32, ix),
+                        _opt(state, "state", win, dt, ix),
+                        _opt(lens, "lens", (R,), torch.int32, ix), yp,
+                        _ptr(state_out, "state_out", win, dt, ix), st), "ola_conv")
     return out, state_out
 
 
@@ -566,40 +596,38 @@ def conv_step(x, w, bias=None, *, state, parent_idx=None, silu=True, out=None, s
     one). Returns (y [R, B, C], state_out [R, B, W-1, C]); state_out may be `state` when
     parent_idx is None."""
     torch = _torch()
-    dev = _first(x, "x", 3)
-    R, B, C = x.shape
-    if w.dim() != 2:
-        raise ValueError("w must be [C, W]")
-    if state.dim() != 4:
-        raise ValueError("state must be [R, Bp, W-1, C]")
-    W, Bp, dt = w.shape[1], state.shape[1], x.dtype
-    with _Scope(dev, stream):
+    ix, code = _first(x, "x", 3)
+    R, B, C = shape = x.shape
+    W, dt, f32 = _taps(w), x.dtype, torch.float32
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise ValueError("state must be a tensor [R, Bp, W-1, C]")
+    Bp = state.shape[1]
+    with _Scope(ix, stream) as st:
         if out is None:
-            out = torch.empty((R, B, C), device=dev, dtype=dt)
+            out = torch.empty(shape, device=x.device, dtype=dt)
         if state_out is None:
-            state_out = torch.empty((R, B, max(W - 1, 0), C), device=dev, dtype=dt)
-        args = [_on(x, "x", (R, B, C), dt, dev, True), _on(w, "w", (C, W), torch.float32, dev),
-                _opt(bias, "bias", (C,), torch.float32, dev),
-                _on(state, "state", (R, Bp, W - 1, C), dt, dev),
-                _opt(parent_idx, "parent_idx", (R, B), torch.int32, dev),
-                _on(out, "out", (R, B, C), dt, dev, True),
-                _on(state_out, "state_out", (R, B, W - 1, C), dt, dev)]
-        d = ConvDesc(R, B, C, W, _dtype_code(dt), int(bool(silu)), *_tok_strides(x),
-                     *_tok_strides(out))
-        _check(ola_conv_step(d, Bp, *args, _stream_ptr(stream)), "ola_conv_step")
+            state_out = torch.empty((R, B, W - 1, C), device=x.device, dtype=dt)
+        xp, x_tok, x_seq = _rows(x, "x", shape, dt, ix)
+        yp, y_tok, y_seq = _rows(out, "out", shape, dt, ix)
+        d = ConvDesc(R, B, C, W, code, bool(silu), x_tok, x_seq, y_tok, y_seq)
+        _check(ola_conv_step(d, Bp, xp, _ptr(w, "w", (C, W), f32, ix),
+                             _opt(bias, "bias", (C,), f32, ix),
+                             _ptr(state, "state", (R, Bp, W - 1, C), dt, ix),
+                             _opt(parent_idx, "parent_idx", (R, B), torch.int32, ix), yp,
+                             _ptr(state_out, "state_out", (R, B, W - 1, C), dt, ix), st),
+               "ola_conv_step")
     return out, state_out
 
 
-def _tokens(x, name, device, dtype):
-    """(pointer, N, token stride) of a tensor [R, P, H, d] whose tokens are evenly spaced."""
-    R, P, H, d = x.shape
-    ptr = _on(x, name, (R, P, H, d), dtype, device, True)
-    tok, seq = _tok_strides(x)
-    if P == 1:
-        tok = seq if R > 1 else tok
+def _tokens(x, name, shape, dtype, index):
+    """(pointer, token stride) of a tensor [R, P, H, d] whose tokens are evenly spaced."""
+    ptr, tok, seq = _rows(x, name, shape, dtype, index)
+    R, P = shape[:2]
+    if P == 1 and R > 1:
+        tok = seq
     elif R > 1 and seq != P * tok:
         raise ValueError(f"{name}: sequences must follow one another at the token stride")
-    return ptr, R * P, tok
+    return ptr, tok
 
 
 def qk_norm(q, k, *, wq=None, wk=None, eps=1e-6, l2=False, positions=None, inv_freq=None,
@@ -610,53 +638,53 @@ def qk_norm(q, k, *, wq=None, wk=None, eps=1e-6, l2=False, positions=None, inv_f
     [R, P] int32 the first `rot` dims are rotated, pairs (i, i + rot/2) or (pair=True)
     (2i, 2i + 1). Returns (q_out, k_out); q_out may be q and k_out may be k."""
     torch = _torch()
-    dev = _first(q, "q", 4)
-    if k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3]:
-        raise ValueError(f"k has shape {tuple(k.shape)}, expected [R, P, Hk, d] as q's")
-    R, P, Hq, d = q.shape
-    Hk, dt = k.shape[2], q.dtype
+    ix, code = _first(q, "q", 4)
+    R, P, Hq, d = qs = q.shape
+    dt, f32 = q.dtype, torch.float32
+    if not isinstance(k, torch.Tensor) or k.dim() != 4 or k.shape[:2] != qs[:2] or \
+            k.shape[3] != d:
+        raise ValueError("k must be a tensor [R, P, Hk, d] with q's R, P and d")
+    ks = k.shape
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
-    rot = 2 * inv_freq.numel() if inv_freq is not None else 0
-    with _Scope(dev, stream):
+    half = inv_freq.numel() if inv_freq is not None else 0
+    with _Scope(ix, stream) as st:
         if q_out is None:
-            q_out = torch.empty((R, P, Hq, d), device=dev, dtype=dt)
+            q_out = torch.empty(qs, device=q.device, dtype=dt)
         if k_out is None:
-            k_out = torch.empty((R, P, Hk, d), device=dev, dtype=dt)
-        if tuple(q_out.shape) != tuple(q.shape) or tuple(k_out.shape) != tuple(k.shape):
-            raise ValueError("q_out and k_out must have the shapes of q and k")
-        qp, N, q_tok = _tokens(q, "q", dev, dt)
-        kp, _, k_tok = _tokens(k, "k", dev, dt)
-        qo, _, qo_tok = _tokens(q_out, "q_out", dev, dt)
-        ko, _, ko_tok = _tokens(k_out, "k_out", dev, dt)
-        args = [qp, kp, _opt(wq, "wq", (d,), torch.float32, dev),
-                _opt(wk, "wk", (d,), torch.float32, dev),
-                _opt(positions, "positions", (R, P), torch.int32, dev),
-                _opt(inv_freq, "inv_freq", (rot // 2,), torch.float32, dev), qo, ko]
-        desc = QkDesc(N, Hq, Hk, d, _dtype_code(dt), int(bool(l2)), rot, int(bool(pair)), eps,
-                      q_tok, k_tok, qo_tok, ko_tok)
-        _check(ola_qk_norm(desc, *args, _stream_ptr(stream)), "ola_qk_norm")
+            k_out = torch.empty(ks, device=q.device, dtype=dt)
+        qp, q_tok = _tokens(q, "q", qs, dt, ix)
+        kp, k_tok = _tokens(k, "k", ks, dt, ix)
+        qo, qo_tok = _tokens(q_out, "q_out", qs, dt, ix)
+        ko, ko_tok = _tokens(k_out, "k_out", ks, dt, ix)
+        desc = QkDesc(R * P, Hq, ks[2], d, code, bool(l2), 2 * half, bool(pair), eps, q_tok, k_tok,
+                      qo_tok, ko_tok)
+        _check(ola_qk_norm(desc, qp, kp, _opt(wq, "wq", (d,), f32, ix),
+                           _opt(wk, "wk", (d,), f32, ix),
+                           _opt(positions, "positions", (R, P), torch.int32, ix),
+                           _opt(inv_freq, "inv_freq", (half,), f32, ix), qo, ko, st),
+               "ola_qk_norm")
     return q_out, k_out
 
 
-def _scan_common(v, dt, A, k, q, D, dt_bias, z, out, softplus, dev):
+def _scan_args(v, dt, A, k, q, D, dt_bias, z, out, softplus, ix, code):
+    """Descriptor of a scan call and its pointers v, dt, A, k, q, D, dt_bias, z, y."""
     torch = _torch()
     f32 = torch.float32
-    R, P, H, d_v = v.shape
-    if k.dim() != 4:
-        raise ValueError("k must be [R, P, G, d_k]")
-    G, d_k, t = k.shape[2], k.shape[3], v.dtype
-    ptrs = dict(v=_on(v, "v", (R, P, H, d_v), t, dev, True),
-                dt=_on(dt, "dt", (R, P, H), f32, dev), A=_on(A, "A", (H,), f32, dev),
-                k=_on(k, "k", (R, P, G, d_k), t, dev, True),
-                q=_on(q, "q", (R, P, G, d_k), t, dev, True),
-                D=_opt(D, "D", (H,), f32, dev), dt_bias=_opt(dt_bias, "dt_bias", (H,), f32, dev),
-                z=_opt(z, "z", (R, P, H, d_v), t, dev, True),
-                y=_on(out, "out", (R, P, H, d_v), t, dev, True))
-    desc = ScanDesc(R, P, H, G, d_k, d_v, _dtype_code(t), int(bool(softplus)), *_tok_strides(v),
-                    *_tok_strides(k), *_tok_strides(q),
-                    *(_tok_strides(z) if z is not None else (0, 0)), *_tok_strides(out))
-    return desc, ptrs
+    R, P, H, d_v = vs = v.shape
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be a tensor [R, P, G, d_k]")
+    G, d_k = k.shape[2:]
+    t, ks, hs = v.dtype, (R, P, G, d_k), (H,)
+    vp, v_tok, v_seq = _rows(v, "v", vs, t, ix)
+    kp, k_tok, k_seq = _rows(k, "k", ks, t, ix)
+    qp, q_tok, q_seq = _rows(q, "q", ks, t, ix)
+    zp, z_tok, z_seq = _opt_rows(z, "z", vs, t, ix)
+    yp, y_tok, y_seq = _rows(out, "out", vs, t, ix)
+    desc = ScanDesc(R, P, H, G, d_k, d_v, code, bool(softplus), v_tok, v_seq, k_tok, k_seq, q_tok,
+                    q_seq, z_tok, z_seq, y_tok, y_seq)
+    return desc, (vp, _ptr(dt, "dt", (R, P, H), f32, ix), _ptr(A, "A", hs, f32, ix), kp, qp,
+                  _opt(D, "D", hs, f32, ix), _opt(dt_bias, "dt_bias", hs, f32, ix), zp), yp
 
 
 def scan(v, dt, A, k, q, *, D=None, dt_bias=None, z=None, S_in=None, lens=None, softplus=True,
@@ -667,23 +695,21 @@ def scan(v, dt, A, k, q, *, D=None, dt_bias=None, z=None, S_in=None, lens=None, 
     Returns (y [R, P, H, d_v], S_out [R, H, d_v, d_k]); rows of `out` behind a sequence's end are
     not written. S_out may be S_in."""
     torch = _torch()
-    dev = _first(v, "v", 4)
-    R, P, H, d_v = v.shape
-    with _Scope(dev, stream):
+    ix, code = _first(v, "v", 4)
+    R, P, H, d_v = vs = v.shape
+    with _Scope(ix, stream) as st:
         if out is None:
-            out = torch.empty((R, P, H, d_v), device=dev, dtype=v.dtype)
-        desc, p = _scan_common(v, dt, A, k, q, D, dt_bias, z, out, softplus, dev)
+            out = torch.empty(vs, device=v.device, dtype=v.dtype)
+        desc, ptrs, yp = _scan_args(v, dt, A, k, q, D, dt_bias, z, out, softplus, ix, code)
         shape = (R, H, d_v, desc.d_k)
         if S_out is None:
-            S_out = torch.empty(shape, device=dev, dtype=torch.float32)
-        s_in = _opt(S_in, "S_in", shape, torch.float32, dev)
-        s_out = _on(S_out, "S_out", shape, torch.float32, dev)
-        len_p = _opt(lens, "lens", (R,), torch.int32, dev)
+            S_out = torch.empty(shape, device=v.device, dtype=torch.float32)
         n = ola_scan_workspace_bytes(desc)
-        ws = torch.empty((n,), device=dev, dtype=torch.uint8) if n else None
-        _check(ola_scan(desc, p["v"], p["dt"], p["A"], p["k"], p["q"], p["D"], p["dt_bias"],
-                        p["z"], s_in, len_p, p["y"], s_out, ws.data_ptr() if n else None, n,
-                        _stream_ptr(stream)), "ola_scan")
+        ws = torch.empty((n,), device=v.device, dtype=torch.uint8) if n else None
+        _check(ola_scan(desc, *ptrs, _opt(S_in, "S_in", shape, torch.float32, ix),
+                        _opt(lens, "lens", (R,), torch.int32, ix), yp,
+                        _ptr(S_out, "S_out", shape, torch.float32, ix),
+                        ws.data_ptr() if n else None, n, st), "ola_scan")
     return out, S_out
 
 
@@ -694,21 +720,21 @@ def scan_step(v, dt, A, k, q, *, state, D=None, dt_bias=None, z=None, parent_idx
     (default: beam b continues state b, or the only one). Returns (y [R, B, H, d_v], state_out
     [R, B, H, d_v, d_k]); state_out may be `state` when parent_idx is None."""
     torch = _torch()
-    dev = _first(v, "v", 4)
-    R, B, H, d_v = v.shape
-    if state.dim() != 5:
-        raise ValueError("state must be [R, Bp, H, d_v, d_k]")
+    ix, code = _first(v, "v", 4)
+    R, B, H, d_v = vs = v.shape
+    if not isinstance(state, torch.Tensor) or state.dim() != 5:
+        raise ValueError("state must be a tensor [R, Bp, H, d_v, d_k]")
     Bp = state.shape[1]
-    with _Scope(dev, stream):
+    with _Scope(ix, stream) as st:
         if out is None:
-            out = torch.empty((R, B, H, d_v), device=dev, dtype=v.dtype)
-        desc, p = _scan_common(v, dt, A, k, q, D, dt_bias, z, out, softplus, dev)
+            out = torch.empty(vs, device=v.device, dtype=v.dtype)
+        desc, ptrs, yp = _scan_args(v, dt, A, k, q, D, dt_bias, z, out, softplus, ix, code)
         if state_out is None:
-            state_out = torch.empty((R, B, H, d_v, desc.d_k), device=dev, dtype=torch.float32)
-        s_in = _on(state, "state", (R, Bp, H, d_v, desc.d_k), torch.float32, dev)
-        s_out = _on(state_out, "state_out", (R, B, H, d_v, desc.d_k), torch.float32, dev)
-        par = _opt(parent_idx, "parent_idx", (R, B), torch.int32, dev)
-        _check(ola_scan_step(desc, Bp, p["v"], p["dt"], p["A"], p["k"], p["q"], p["D"],
-                             p["dt_bias"], p["z"], s_in, par, p["y"], s_out,
-                             _stream_ptr(stream)), "ola_scan_step")
+            state_out = torch.empty((R, B, H, d_v, desc.d_k), device=v.device,
+                                    dtype=torch.float32)
+        _check(ola_scan_step(desc, Bp, *ptrs,
+                             _ptr(state, "state", (R, Bp, H, d_v, desc.d_k), torch.float32, ix),
+                             _opt(parent_idx, "parent_idx", (R, B), torch.int32, ix), yp,
+                             _ptr(state_out, "state_out", (R, B, H, d_v, desc.d_k),
+                                  torch.float32, ix), st), "ola_scan_step")
     return out, state_out

@@ -3,40 +3,96 @@
 //     y[p][c] = act(bias[c] + sum_{i<W} w[c][i] u[p + i][c]),   u = (W-1 earlier tokens) ++ x
 //
 // 2W + a few operations per element against one read and one write of it: the bound is HBM. A
-// thread owns 16 bytes of neighbouring channels, keeps their W taps in registers and walks
-// consecutive tokens with the window of the last W-1 inputs in registers, so an element is read
-// once (plus the W-1 tokens before each thread's stretch, which its neighbour's reads leave in
-// L2). The window's values are moved, never recomputed: the state that leaves is the input's bits.
+// thread owns 16 bytes of neighbouring channels and walks consecutive tokens with the window of
+// the last W-1 inputs in registers, so an element is read once (plus the W-1 tokens before each
+// thread's stretch, which its neighbour's reads leave in L2). The block brings its channels' taps
+// in once, transposed through shared memory ([tap][channel], read 16 bytes at a time); sums run two
+// channels per instruction. The window's values are moved, never recomputed: the state that leaves
+// is the input's bits.
 #include "ola_layer.cuh"
 
 namespace ola {
 
 namespace {
 
-constexpr int kConvThreads = 128;
+constexpr int kConvThreads = 256;
 constexpr int kConvUnroll = 4;      // tokens loaded together
 
+// fp32 pairs of a pack: VEC elements as (VEC + 1) / 2 pairs.
+template <typename T, int VEC>
+struct Pairs {
+  static constexpr int N = (VEC + 1) / 2;
+  uint64_t p[N];
+  __device__ __forceinline__ void from(const Pack<T, VEC>& k) {
+    float f[VEC];
+    k.unpack(f);
+#pragma unroll
+    for (int e = 0; e < N; ++e) p[e] = f2(f[2 * e], VEC > 1 ? f[VEC > 1 ? 2 * e + 1 : 0] : 0.f);
+  }
+  __device__ __forceinline__ void to(Pack<T, VEC>& k) const {
+    float f[VEC];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float2 t = un2(p[e]);
+      f[2 * e] = t.x;
+      if (VEC > 1) f[VEC > 1 ? 2 * e + 1 : 0] = t.y;
+    }
+    k.pack(f);
+  }
+};
+
+// Taps and biases of a thread's channels.
 template <typename T, int VEC, int W>
 struct Taps {
-  float w[W][VEC], b[VEC];
-  __device__ __forceinline__ void load(const ConvArgs& a, int c) {
+  static constexpr int N = (VEC + 1) / 2;
+  uint64_t w[W][N], b[N];
+
+  // Cooperative: the taps of the block's channels c0 .. c0 + nc - 1 go through shared memory.
+  __device__ __forceinline__ void load(const ConvArgs& a, float* sm, int c0, int nc, int cl) {
+    const int tid = threadIdx.y * blockDim.x + threadIdx.x;
+    const int have = min(nc, a.C - c0);
+    for (int i = tid; i < have * W; i += kConvThreads)
+      sm[(i % W) * nc + i / W] = __ldg(a.w + int64_t(c0) * W + i);
+    for (int i = tid; i < have; i += kConvThreads)
+      sm[W * nc + i] = a.bias ? __ldg(a.bias + c0 + i) : 0.f;
+    __syncthreads();
+    if (cl >= have) return;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
+    for (int i = 0; i <= W; ++i) {
+      float f[VEC];
+      const float* src = sm + i * nc + cl;
+      if constexpr (VEC >= 4) {
 #pragma unroll
-      for (int i = 0; i < W; ++i) w[i][e] = __ldg(a.w + size_t(c + e) * W + i);
-      b[e] = a.bias ? __ldg(a.bias + c + e) : 0.f;
+        for (int q = 0; q < VEC / 4; ++q) {
+          const float4 t = reinterpret_cast<const float4*>(src)[q];
+          f[4 * q] = t.x;
+          f[4 * q + 1] = t.y;
+          f[4 * q + 2] = t.z;
+          f[4 * q + 3] = t.w;
+        }
+      } else {
+        f[0] = src[0];
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const uint64_t v = f2(f[2 * e], VEC > 1 ? f[VEC > 1 ? 2 * e + 1 : 0] : 0.f);
+        if (i < W)
+          w[i < W ? i : 0][e] = v;
+        else
+          b[e] = v;
+      }
     }
   }
   // win[0..W-2] the earlier tokens, oldest first, x the newest
-  __device__ __forceinline__ void apply(const float (&win)[W - 1][VEC], const float (&x)[VEC],
-                                        int silu, float (&y)[VEC]) const {
+  __device__ __forceinline__ void apply(const Pairs<T, VEC> (&win)[W - 1], const Pairs<T, VEC>& x,
+                                        int silu, Pairs<T, VEC>& y) const {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      float u = b[e];
+    for (int e = 0; e < N; ++e) {
+      uint64_t u = b[e];
 #pragma unroll
-      for (int i = 0; i < W - 1; ++i) u = fmaf(w[i][e], win[i][e], u);
-      u = fmaf(w[W - 1][e], x[e], u);
-      y[e] = silu ? silu_f<T>(u) : u;
+      for (int i = 0; i < W - 1; ++i) u = fma2(w[i][e], win[i].p[e], u);
+      u = fma2(w[W - 1][e], x.p[e], u);
+      y.p[e] = silu ? silu2<T>(u) : u;
     }
   }
 };
@@ -44,11 +100,14 @@ struct Taps {
 // blockDim = (channel vectors, token stretches); grid.x = channel blocks x token blocks x R.
 template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvArgs a) {
+  extern __shared__ __align__(16) float sm[];
   const int ct = blockIdx.x % a.n_ctile;
   const int rest = blockIdx.x / a.n_ctile;
   const int r = rest / a.n_ttile;
   const int64_t tile = int64_t(rest % a.n_ttile) * blockDim.y + threadIdx.y;
-  const int c = (ct * blockDim.x + threadIdx.x) * VEC;
+  const int nc = blockDim.x * VEC, c0 = ct * nc, cl = threadIdx.x * VEC, c = c0 + cl;
+  Taps<T, VEC, W> taps;
+  taps.load(a, sm, c0, nc, cl);
   const int64_t t0w = tile * a.tt;
   if (c >= a.C || (t0w >= a.P && tile > 0)) return;
   const int t0 = int(t0w);
@@ -60,14 +119,14 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvArgs a) {
   const T* si = a.state_in
                     ? static_cast<const T*>(a.state_in) + int64_t(r) * (W - 1) * a.C + c
                     : nullptr;
-  float win[W - 1][VEC];
+  Pairs<T, VEC> win[W - 1];
   if (t0 == 0) {
     Pack<T, VEC> keep[W - 1];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
       keep[j].zero();
       if (si) keep[j].load(si + int64_t(j) * a.C);
-      keep[j].unpack(win[j]);
+      win[j].from(keep[j]);
     }
     if (a.state_out) {
       // the last W-1 tokens of state ++ x[:L]; every read precedes the first write, so that
@@ -95,11 +154,9 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvArgs a) {
     for (int j = 0; j < W - 1; ++j) {             // tt >= W - 1: these tokens exist
       Pack<T, VEC> p;
       p.load(x + int64_t(t0 + j - (W - 1)) * a.x_tok);
-      p.unpack(win[j]);
+      win[j].from(p);
     }
   }
-  Taps<T, VEC, W> taps;
-  taps.load(a, c);
   for (int t = t0; t < t1; t += kConvUnroll) {
     Pack<T, VEC> in[kConvUnroll];
 #pragma unroll
@@ -110,19 +167,15 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvArgs a) {
 #pragma unroll
     for (int i = 0; i < kConvUnroll; ++i) {
       if (t + i >= t1) break;
-      float xf[VEC], yf[VEC];
-      in[i].unpack(xf);
+      Pairs<T, VEC> xf, yf;
+      xf.from(in[i]);
       taps.apply(win, xf, a.silu, yf);
       Pack<T, VEC> o;
-      o.pack(yf);
+      yf.to(o);
       o.store(y + int64_t(t + i) * a.y_tok);
 #pragma unroll
-      for (int j = 0; j < W - 2; ++j) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
-      }
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) win[W - 2][e] = xf[e];
+      for (int j = 0; j < W - 2; ++j) win[j] = win[j + 1];
+      win[W - 2] = xf;
     }
   }
 }
@@ -130,44 +183,58 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvArgs a) {
 // One token of every beam: thread = 16 bytes of channels x tt consecutive beams (of all requests).
 template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvArgs a) {
+  extern __shared__ __align__(16) float sm[];
   const int ct = blockIdx.x % a.n_ctile;
   const int64_t tile = int64_t(blockIdx.x / a.n_ctile) * blockDim.y + threadIdx.y;
-  const int c = (ct * blockDim.x + threadIdx.x) * VEC;
+  const int nc = blockDim.x * VEC, c0 = ct * nc, cl = threadIdx.x * VEC, c = c0 + cl;
   const int64_t n = int64_t(a.R) * a.P;
   const int64_t i0 = tile * a.tt, i1 = min(i0 + a.tt, n);
-  if (c >= a.C || i0 >= i1) return;
   Taps<T, VEC, W> taps;
-  taps.load(a, c);
-  for (int64_t i = i0; i < i1; ++i) {
-    const int r = int(i / a.P), b = int(i - int64_t(r) * a.P);
-    const int p = parent_state(a.parent, r, b, a.P, a.Bp, a.err);
-    const T* si = static_cast<const T*>(a.state_in) +
-                  (int64_t(r) * a.Bp + p) * (W - 1) * a.C + c;
-    Pack<T, VEC> s[W - 1], x;
+  taps.load(a, sm, c0, nc, cl);
+  if (c >= a.C || i0 >= i1) return;
+  for (int64_t i = i0; i < i1; i += 2) {           // two beams' loads together
+    Pack<T, VEC> s[2][W - 1], x[2];
+    int64_t yo[2];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) s[j].load(si + int64_t(j) * a.C);
-    x.load(static_cast<const T*>(a.x) + int64_t(r) * a.x_seq + int64_t(b) * a.x_tok + c);
-    float win[W - 1][VEC], xf[VEC], yf[VEC];
+    for (int u = 0; u < 2; ++u) {
+      x[u].zero();
+      yo[u] = -1;
+      if (i + u >= i1) continue;
+      const int r = int((i + u) / a.P), b = int(i + u - int64_t(r) * a.P);
+      const int p = parent_state(a.parent, r, b, a.P, a.Bp, a.err);
+      const T* si = static_cast<const T*>(a.state_in) +
+                    (int64_t(r) * a.Bp + p) * (W - 1) * a.C + c;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) s[j].unpack(win[j]);
-    x.unpack(xf);
-    taps.apply(win, xf, a.silu, yf);
-    Pack<T, VEC> o;
-    o.pack(yf);
-    o.store(static_cast<T*>(a.y) + int64_t(r) * a.y_seq + int64_t(b) * a.y_tok + c);
-    T* so = static_cast<T*>(a.state_out) + i * (W - 1) * a.C + c;
+      for (int j = 0; j < W - 1; ++j) s[u][j].load(si + int64_t(j) * a.C);
+      x[u].load(static_cast<const T*>(a.x) + int64_t(r) * a.x_seq + int64_t(b) * a.x_tok + c);
+      yo[u] = int64_t(r) * a.y_seq + int64_t(b) * a.y_tok + c;
+    }
 #pragma unroll
-    for (int j = 0; j < W - 2; ++j) s[j + 1].store(so + int64_t(j) * a.C);
-    x.store(so + int64_t(W - 2) * a.C);
+    for (int u = 0; u < 2; ++u) {
+      if (yo[u] < 0) break;
+      Pairs<T, VEC> win[W - 1], xf, yf;
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) win[j].from(s[u][j]);
+      xf.from(x[u]);
+      taps.apply(win, xf, a.silu, yf);
+      Pack<T, VEC> o;
+      yf.to(o);
+      o.store(static_cast<T*>(a.y) + yo[u]);
+      T* so = static_cast<T*>(a.state_out) + (i + u) * (W - 1) * a.C + c;
+#pragma unroll
+      for (int j = 0; j < W - 2; ++j) s[u][j + 1].store(so + int64_t(j) * a.C);
+      x[u].store(so + int64_t(W - 2) * a.C);
+    }
   }
 }
 
 template <typename T, int VEC, int W>
 cudaError_t run(const ConvArgs& a, bool step, dim3 block, unsigned grid, cudaStream_t st) {
+  const size_t smem = sizeof(float) * (W + 1) * block.x * VEC;
   if (step)
-    conv_step_kernel<T, VEC, W><<<grid, block, 0, st>>>(a);
+    conv_step_kernel<T, VEC, W><<<grid, block, smem, st>>>(a);
   else
-    conv_kernel<T, VEC, W><<<grid, block, 0, st>>>(a);
+    conv_kernel<T, VEC, W><<<grid, block, smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -185,20 +252,22 @@ cudaError_t launch(ConvArgs a, int in_dtype, int W, bool wide, bool step, cudaSt
   if (e != cudaSuccess) return e;
   const int vec = wide ? (in_dtype == OLA_BF16 ? 8 : 4) : 1;
   const int64_t nvec = (int64_t(a.C) + vec - 1) / vec;
+  // a warp's width of channel vectors (512 bytes of a row): wider blocks would bring in more taps
+  // for the same tokens
   int bx = 8;
-  while (bx < kConvThreads && bx < nvec) bx *= 2;
+  while (bx < 32 && bx < nvec) bx *= 2;
   const int by = kConvThreads / bx;
   a.n_ctile = int((nvec + bx - 1) / bx);
-  // tokens (beams) per thread: as many as leave about 16 blocks of 128 threads for every SM
+  // tokens (beams) per thread: as many as leave about 8 blocks for every SM
   const int64_t rows = step ? int64_t(a.R) * a.P : a.P;
   const int64_t seqs = step ? 1 : a.R;
-  a.tt = step ? 8 : 32;
-  const int least = step ? 1 : 4;
+  a.tt = step ? 16 : 32;
+  const int least = step ? 2 : 4;
   auto blocks = [&](int tt) {
     const int64_t n = (rows + int64_t(tt) * by - 1) / (int64_t(tt) * by);
     return (n < 1 ? 1 : n) * seqs * a.n_ctile;
   };
-  while (a.tt > least && blocks(a.tt) < int64_t(16) * sms) a.tt /= 2;
+  while (a.tt > least && blocks(a.tt) < int64_t(8) * sms) a.tt /= 2;
   const int64_t grid = blocks(a.tt);
   a.n_ttile = int(grid / seqs / a.n_ctile);
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;

@@ -6,9 +6,10 @@
 // A head is read once and written once: the bound is HBM. A group of GL lanes owns a head: each
 // lane holds items of two 16-byte chunks. An item is one rotation pair of chunks (j, j + rot/2)
 // or two neighbouring chunks, so a rotation never leaves its lane; the sum of squares is joined by
-// shuffles. A warp takes one token's heads 32 / GL at a time; the token's angles are worked out
-// once, each by one of the groups, and handed round by shuffles. Angles are reduced in fp64:
-// position * inv_freq in fp32 would be off by 2^-24 of up to 10^5 radians.
+// shuffles. A warp takes one token's heads 32 / GL at a time and walks over tokens, with its
+// weights in registers. The token's angles are worked out once, one per lane, and handed round
+// through shared memory. Angles are reduced in fp64: position * inv_freq in fp32 would be off by
+// 2^-24 of up to 10^5 radians.
 #include "ola_layer.cuh"
 
 namespace ola {
@@ -21,15 +22,19 @@ constexpr int kQkThreads = 128;
 template <typename T, int GL, int NI, bool PAIR>
 __global__ void __launch_bounds__(kQkThreads) qk_norm_kernel(QkArgs a) {
   constexpr int E = 16 / int(sizeof(T));          // elements per chunk
+  constexpr int H2 = E / 2;                       // fp32 pairs per chunk
   constexpr int NG = 32 / GL;                     // heads a warp takes together
+  extern __shared__ __align__(16) float sm[];     // per warp: cos and sin of rot / 2 angles
   const int lane = threadIdx.x & 31, gl = lane % GL, grp = lane / GL;
-  const int64_t warp = (int64_t(blockIdx.x) * kQkThreads + threadIdx.x) >> 5;
-  const int64_t tok = warp / a.hsplit;
-  const int part = int(warp % a.hsplit);
-  if (tok >= a.N) return;                         // whole warps
+  const int nwarp = gridDim.x * (kQkThreads / 32);
+  const int64_t w0 = int64_t(blockIdx.x) * (kQkThreads / 32) + (threadIdx.x >> 5);
+  const int nang = (a.rot / 2 + 31) / 32 * 32;    // table entries, filled up with no rotation
+  float* ct = sm + (threadIdx.x >> 5) * 2 * nang;
+  float* st = ct + nang;
   const int nch = a.d / E, half = a.rot / (2 * E), nitem = (nch + 1) / 2;
   // chunks of this lane's items; -1: none
   int c0[NI], c1[NI];
+  uint64_t wq0[NI][H2], wq1[NI][H2], wk0[NI][H2], wk1[NI][H2];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int j = gl + i * GL;
@@ -42,118 +47,150 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_kernel(QkArgs a) {
     }
     if (j >= nitem) c0[i] = c1[i] = -1;
     if (c1[i] >= nch) c1[i] = -1;
+#pragma unroll
+    for (int e = 0; e < H2; ++e) {
+      auto pair = [&](const float* w, int ch) {
+        return w && ch >= 0 ? f2(__ldg(w + ch * E + 2 * e), __ldg(w + ch * E + 2 * e + 1))
+                            : f2(1.f, 1.f);
+      };
+      wq0[i][e] = pair(a.wq, c0[i]);
+      wq1[i][e] = pair(a.wq, c1[i]);
+      wk0[i][e] = pair(a.wk, c0[i]);
+      wk1[i][e] = pair(a.wk, c1[i]);
+    }
   }
-  // cos and sin of the E angles of each item: E pairs of chunks (j, j + half), or E / 2 pairs
-  // inside each of the two chunks. Group g works out the angles e = g, g + NG, ...
-  float cs[NI][E], sn[NI][E];
-  if (a.rot) {
-    const double pos = double(__ldg(a.pos + tok));
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int j = gl + i * GL;
-      float mc[(E + NG - 1) / NG], ms[(E + NG - 1) / NG];
-#pragma unroll
-      for (int m = 0; m < (E + NG - 1) / NG; ++m) {
-        const int f = j * E + m * NG + grp;       // the same index in both pairings
-        mc[m] = 1.f;
-        ms[m] = 0.f;
-        if (f < a.rot / 2 && m * NG + grp < E) {
+  const int uq = (a.Hq + NG - 1) / NG, uk = (a.Hk + NG - 1) / NG;   // head groups
+  const int per = (uq + uk + a.hsplit - 1) / a.hsplit;
+  const float inv_d = 1.f / float(a.d);
+  for (int64_t w = w0; w < a.N * a.hsplit; w += nwarp) {
+    const int64_t tok = w / a.hsplit;
+    const int part = int(w - tok * a.hsplit);
+    if (a.rot) {
+      __syncwarp();
+      const double pos = double(__ldg(a.pos + tok));
+      for (int f = lane; f < nang; f += 32) {
+        float c = 1.f, s = 0.f;
+        if (f < a.rot / 2) {
           double turns = pos * double(__ldg(a.inv_freq + f)) * 0.15915494309189533577;
           turns -= rint(turns);
-          sincospif(float(2.0 * turns), &ms[m], &mc[m]);
+          sincospif(float(2.0 * turns), &s, &c);
+        }
+        ct[f] = c;
+        st[f] = s;
+      }
+      __syncwarp();
+    }
+    // cos, sin of an item's E angles: E pairs of chunks (j, j + half), or E / 2 pairs inside each
+    // of the two chunks; item j holds the angles j E .. j E + E - 1 in both
+    uint64_t cs[NI][H2], sn[NI][H2];
+    if (a.rot) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int f = (gl + i * GL) * E;
+#pragma unroll
+        for (int e = 0; e < H2; e += 2) {
+          ulonglong2 c2 = make_ulonglong2(0, 0), s2 = c2;
+          if (f < nang) {
+            c2 = *reinterpret_cast<const ulonglong2*>(ct + f + 2 * e);
+            s2 = *reinterpret_cast<const ulonglong2*>(st + f + 2 * e);
+          }
+          cs[i][e] = c2.x;
+          sn[i][e] = s2.x;
+          cs[i][e + 1] = c2.y;
+          sn[i][e + 1] = s2.y;
         }
       }
+    }
+    const int u1 = min(uq + uk, (part + 1) * per);
+    for (int u = part * per; u < u1; ++u) {
+      const bool isq = u < uq;
+      const int h = (isq ? u : u - uq) * NG + grp;
+      const bool on = h < (isq ? a.Hq : a.Hk);
+      const T* src = (isq ? static_cast<const T*>(a.q) + tok * a.q_tok
+                          : static_cast<const T*>(a.k) + tok * a.k_tok) + int64_t(h) * a.d;
+      T* dst = (isq ? static_cast<T*>(a.q_out) + tok * a.qo_tok
+                    : static_cast<T*>(a.k_out) + tok * a.ko_tok) + int64_t(h) * a.d;
+      Pack<T, E> r0[NI], r1[NI];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        cs[i][e] = __shfl_sync(kFull, mc[e / NG], (e % NG) * GL + gl);
-        sn[i][e] = __shfl_sync(kFull, ms[e / NG], (e % NG) * GL + gl);
+      for (int i = 0; i < NI; ++i) {
+        r0[i].zero();
+        r1[i].zero();
+        if (on && c0[i] >= 0) r0[i].load(src + c0[i] * E);
+        if (on && c1[i] >= 0) r1[i].load(src + c1[i] * E);
       }
-    }
-  }
-  const int heads = a.Hq + a.Hk;
-  const int per = ((heads + a.hsplit - 1) / a.hsplit + NG - 1) / NG * NG;
-  const int h1 = min(heads, (part + 1) * per);
-  for (int hb = part * per; hb < h1; hb += NG) {
-    const int h = hb + grp;
-    const bool on = h < h1;
-    const bool isq = h < a.Hq;
-    const T* src = isq ? static_cast<const T*>(a.q) + tok * a.q_tok + int64_t(h) * a.d
-                       : static_cast<const T*>(a.k) + tok * a.k_tok + int64_t(h - a.Hq) * a.d;
-    T* dst = isq ? static_cast<T*>(a.q_out) + tok * a.qo_tok + int64_t(h) * a.d
-                 : static_cast<T*>(a.k_out) + tok * a.ko_tok + int64_t(h - a.Hq) * a.d;
-    const float* w = isq ? a.wq : a.wk;
-    Pack<T, E> r0[NI], r1[NI];
+      uint64_t x0[NI][H2], x1[NI][H2], s2 = f2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      r0[i].zero();
-      r1[i].zero();
-      if (on && c0[i] >= 0) r0[i].load(src + c0[i] * E);
-      if (on && c1[i] >= 0) r1[i].load(src + c1[i] * E);
-    }
-    float s = 0.f;
+      for (int i = 0; i < NI; ++i) {
+        float f0[E], f1[E];
+        r0[i].unpack(f0);
+        r1[i].unpack(f1);
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      float x0[E], x1[E];
-      r0[i].unpack(x0);
-      r1[i].unpack(x1);
-#pragma unroll
-      for (int e = 0; e < E; ++e) s = fmaf(x0[e], x0[e], fmaf(x1[e], x1[e], s));
-    }
-#pragma unroll
-    for (int o = GL / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-    const float rs = rsqrtf((a.l2 ? s : s / float(a.d)) + a.eps);
-    if (!on) continue;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      if (c0[i] < 0) continue;
-      float x0[E], x1[E];
-      r0[i].unpack(x0);
-      r1[i].unpack(x1);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        x0[e] *= rs;
-        x1[e] *= rs;
-      }
-      if (w) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          x0[e] *= __ldg(w + c0[i] * E + e);
-          if (c1[i] >= 0) x1[e] *= __ldg(w + c1[i] * E + e);
+        for (int e = 0; e < H2; ++e) {
+          x0[i][e] = f2(f0[2 * e], f0[2 * e + 1]);
+          x1[i][e] = f2(f1[2 * e], f1[2 * e + 1]);
+          s2 = fma2(x0[i][e], x0[i][e], fma2(x1[i][e], x1[i][e], s2));
         }
       }
-      if (a.rot) {
+      const float2 st2 = un2(s2);
+      float s = st2.x + st2.y;
+#pragma unroll
+      for (int o = GL / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+      const float rs = rsqrtf((a.l2 ? s : s * inv_d) + a.eps);
+      if (!on) continue;
+      const uint64_t rs2 = f2(rs, rs);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        if (c0[i] < 0) continue;
+#pragma unroll
+        for (int e = 0; e < H2; ++e) {
+          x0[i][e] = mul2(mul2(x0[i][e], rs2), isq ? wq0[i][e] : wk0[i][e]);
+          x1[i][e] = mul2(mul2(x1[i][e], rs2), isq ? wq1[i][e] : wk1[i][e]);
+        }
         if (!PAIR) {
           if (c0[i] < half) {
+            const uint64_t neg = f2(-1.f, -1.f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-              const float p = x0[e], q = x1[e];
-              x0[e] = p * cs[i][e] - q * sn[i][e];
-              x1[e] = q * cs[i][e] + p * sn[i][e];
+            for (int e = 0; e < H2; ++e) {
+              const uint64_t p = x0[i][e], q = x1[i][e];
+              x0[i][e] = fma2(p, cs[i][e], mul2(mul2(q, sn[i][e]), neg));
+              x1[i][e] = fma2(q, cs[i][e], mul2(p, sn[i][e]));
             }
           }
-        } else {
+        } else if (c0[i] * E < a.rot) {
           // rot is a multiple of 16, so a chunk is rotated as a whole or not at all
+          const bool both = c1[i] * E < a.rot;
 #pragma unroll
-          for (int e = 0; e < E / 2; ++e) {
-            if (c0[i] * E < a.rot) {
-              const float p = x0[2 * e], q = x0[2 * e + 1];
-              x0[2 * e] = p * cs[i][e] - q * sn[i][e];
-              x0[2 * e + 1] = q * cs[i][e] + p * sn[i][e];
-            }
-            if (c1[i] * E < a.rot) {
-              const float p = x1[2 * e], q = x1[2 * e + 1];
-              x1[2 * e] = p * cs[i][E / 2 + e] - q * sn[i][E / 2 + e];
-              x1[2 * e + 1] = q * cs[i][E / 2 + e] + p * sn[i][E / 2 + e];
-            }
+          for (int e = 0; e < H2; ++e) {
+            // pair e of chunk 0 has angle e, of chunk 1 angle E / 2 + e
+            auto turn = [&](uint64_t v, int k) {
+              const float2 c2 = un2(cs[i][k / 2]), t2 = un2(sn[i][k / 2]), xy = un2(v);
+              const float c = k & 1 ? c2.y : c2.x, t = k & 1 ? t2.y : t2.x;
+              return f2(xy.x * c - xy.y * t, xy.y * c + xy.x * t);
+            };
+            x0[i][e] = turn(x0[i][e], e);
+            if (both) x1[i][e] = turn(x1[i][e], H2 + e);
           }
         }
-      }
-      Pack<T, E> o;
-      o.pack(x0);
-      o.store(dst + c0[i] * E);
-      if (c1[i] >= 0) {
-        o.pack(x1);
-        o.store(dst + c1[i] * E);
+        float f[E];
+        Pack<T, E> o;
+#pragma unroll
+        for (int e = 0; e < H2; ++e) {
+          const float2 t = un2(x0[i][e]);
+          f[2 * e] = t.x;
+          f[2 * e + 1] = t.y;
+        }
+        o.pack(f);
+        o.store(dst + c0[i] * E);
+        if (c1[i] >= 0) {
+#pragma unroll
+          for (int e = 0; e < H2; ++e) {
+            const float2 t = un2(x1[i][e]);
+            f[2 * e] = t.x;
+            f[2 * e + 1] = t.y;
+          }
+          o.pack(f);
+          o.store(dst + c1[i] * E);
+        }
       }
     }
   }
@@ -161,10 +198,11 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_kernel(QkArgs a) {
 
 template <typename T, int GL, int NI>
 cudaError_t run(const QkArgs& a, int pair, unsigned grid, cudaStream_t st) {
+  const size_t smem = sizeof(float) * 2 * ((a.rot / 2 + 31) / 32 * 32) * (kQkThreads / 32);
   if (pair)
-    qk_norm_kernel<T, GL, NI, true><<<grid, kQkThreads, 0, st>>>(a);
+    qk_norm_kernel<T, GL, NI, true><<<grid, kQkThreads, smem, st>>>(a);
   else
-    qk_norm_kernel<T, GL, NI, false><<<grid, kQkThreads, 0, st>>>(a);
+    qk_norm_kernel<T, GL, NI, false><<<grid, kQkThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -180,12 +218,12 @@ cudaError_t launch_qk_norm(QkArgs a, int in_dtype, int pair, cudaStream_t st) {
   while (gl < 32 && gl < nitem) gl *= 2;
   const int ng = 32 / gl;
   // few tokens: their heads are shared out over more warps, down to one head group each
-  const int groups = (a.Hq + a.Hk + ng - 1) / ng;
+  const int groups = (a.Hq + ng - 1) / ng + (a.Hk + ng - 1) / ng;
   a.hsplit = 1;
   while (a.hsplit < groups && a.N * a.hsplit < int64_t(16) * sms) a.hsplit *= 2;
-  const int64_t warps = a.N * a.hsplit;
-  const int64_t grid = (warps * 32 + kQkThreads - 1) / kQkThreads;
-  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  // enough blocks to fill the machine; each warp walks on from token to token
+  int64_t grid = (a.N * a.hsplit * 32 + kQkThreads - 1) / kQkThreads;
+  if (grid > int64_t(sms) * 8) grid = int64_t(sms) * 8;
   const unsigned g = unsigned(grid);
   if (in_dtype == OLA_BF16) {
     if (gl == 1) return run<__nv_bfloat16, 1, 1>(a, pair, g, st);

@@ -75,12 +75,6 @@ struct ChunkScan {
   int ntile;                            // blocks of 64 value columns
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -88,37 +82,6 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Two fp32 at a time (fma.rn.f32x2): half the instructions of the scalar forms.
-__device__ __forceinline__ uint64_t f2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t u2(uint32_t a, uint32_t b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ float2 un2(uint64_t a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ uint32_t pack2(uint64_t a) {
   const float2 f = un2(a);
   return pack2(f.x, f.y);
@@ -766,8 +729,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               if (GATE)
-                o[e] = mul2(o[e], f2(silu_f<__nv_bfloat16>(lo_f(zw[e])),
-                                     silu_f<__nv_bfloat16>(hi_f(zw[e]))));
+                o[e] = mul2(o[e], silu2<__nv_bfloat16>(u2(zw[e] << 16, zw[e] & 0xffff0000u)));
               ow[e] = pack2(o[e]);
             }
             const uint4 o4 = make_uint4(ow[0], ow[1], ow[2], ow[3]);
