@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kConvThreads = 256;
 constexpr int kConvUnroll = 4;      // tokens loaded together
+constexpr int kAhead = 3;           // groups of them in flight
 
 // fp32 pairs of a pack: VEC elements as (VEC + 1) / 2 pairs.
 template <typename T, int VEC>
@@ -106,15 +107,33 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvArgs a) {
   const int r = rest / a.n_ttile;
   const int64_t tile = int64_t(rest % a.n_ttile) * blockDim.y + threadIdx.y;
   const int nc = blockDim.x * VEC, c0 = ct * nc, cl = threadIdx.x * VEC, c = c0 + cl;
-  Taps<T, VEC, W> taps;
-  taps.load(a, sm, c0, nc, cl);
   const int64_t t0w = tile * a.tt;
-  if (c >= a.C || (t0w >= a.P && tile > 0)) return;
-  const int t0 = int(t0w);
+  const bool active = c < a.C && (t0w < a.P || tile == 0);
+  const int t0 = active ? int(t0w) : 0;
   const int L = seq_len(a.lens, r, a.P);
-  const int t1 = min(t0 + a.tt, L);
+  const int t1 = active ? min(t0 + a.tt, L) : 0;
   const T* x = static_cast<const T*>(a.x) + int64_t(r) * a.x_seq + c;
   T* y = static_cast<T*>(a.y) + int64_t(r) * a.y_seq + c;
+  // 16-byte vectors come through a ring of kAhead groups of tokens in shared memory, which every
+  // thread fills for itself: deep prefetch without registers and without barriers
+  constexpr bool ASYNC = VEC * sizeof(T) == 16;
+  T* ring = reinterpret_cast<T*>(sm + (W + 1) * nc) +
+            size_t(threadIdx.y * blockDim.x + threadIdx.x) * VEC;
+  auto fetch_async = [&](int t, int slot) {
+    if constexpr (ASYNC) {
+#pragma unroll
+      for (int i = 0; i < kConvUnroll; ++i)
+        if (t + i < t1)
+          cp_async16(ring + size_t(slot * kConvUnroll + i) * kConvThreads * VEC,
+                     x + int64_t(t + i) * a.x_tok);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s) fetch_async(t0 + s * kConvUnroll, s);
+  Taps<T, VEC, W> taps;
+  taps.load(a, sm, c0, nc, cl);
+  if (!active) return;
   // the window before the stretch: earlier tokens, or the incoming state
   const T* si = a.state_in
                     ? static_cast<const T*>(a.state_in) + int64_t(r) * (W - 1) * a.C + c
@@ -157,13 +176,21 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvArgs a) {
       win[j].from(p);
     }
   }
+  int slot = 0;
   for (int t = t0; t < t1; t += kConvUnroll) {
     Pack<T, VEC> in[kConvUnroll];
+    if constexpr (ASYNC) asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
 #pragma unroll
     for (int i = 0; i < kConvUnroll; ++i) {
-      in[i].zero();
-      if (t + i < t1) in[i].load(x + int64_t(t + i) * a.x_tok);
+      if constexpr (ASYNC) {
+        in[i].load(ring + size_t(slot * kConvUnroll + i) * kConvThreads * VEC);
+      } else {
+        in[i].zero();
+        if (t + i < t1) in[i].load(x + int64_t(t + i) * a.x_tok);
+      }
     }
+    fetch_async(t + kAhead * kConvUnroll, slot);
+    slot = slot + 1 < kAhead ? slot + 1 : 0;
 #pragma unroll
     for (int i = 0; i < kConvUnroll; ++i) {
       if (t + i >= t1) break;
@@ -231,10 +258,21 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvArgs a) {
 template <typename T, int VEC, int W>
 cudaError_t run(const ConvArgs& a, bool step, dim3 block, unsigned grid, cudaStream_t st) {
   const size_t smem = sizeof(float) * (W + 1) * block.x * VEC;
-  if (step)
+  if (step) {
     conv_step_kernel<T, VEC, W><<<grid, block, smem, st>>>(a);
-  else
-    conv_kernel<T, VEC, W><<<grid, block, smem, st>>>(a);
+  } else {
+    constexpr size_t ring =
+        VEC * sizeof(T) == 16 ? size_t(kAhead) * kConvUnroll * kConvThreads * 16 : 0;
+    if (smem + ring > 48 * 1024) {
+      static std::atomic<uint64_t> done{0};
+      cudaError_t e = once_per_device(done, [] {
+        return cudaFuncSetAttribute(conv_kernel<T, VEC, W>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+      });
+      if (e != cudaSuccess) return e;
+    }
+    conv_kernel<T, VEC, W><<<grid, block, smem + ring, st>>>(a);
+  }
   return cudaGetLastError();
 }
 

@@ -126,7 +126,11 @@ template <typename T>
 __device__ __forceinline__ float silu_f(float u);
 template <>
 __device__ __forceinline__ float silu_f<float>(float u) {
-  return u / (1.f + expf(-u));
+  // the approximate reciprocal and one Newton step (within two units of 2^-23); the exponent's
+  // limit keeps the denominator finite (SiLU below -88 is 0 to within 2^-118)
+  const float d = 1.f + expf(fminf(-u, 88.f));
+  const float r = rcp(d);
+  return u * fmaf(r, fmaf(-d, r, 1.f), r);
 }
 template <>
 __device__ __forceinline__ float silu_f<__nv_bfloat16>(float u) {
@@ -157,8 +161,7 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
-// VEC consecutive elements as they lie in memory: one 16-byte word (VEC * sizeof(T) = 16) or one
-// element (VEC = 1).
+// VEC consecutive elements as they lie in memory: one 16- or 8-byte word or one element (VEC = 1).
 template <typename T, int VEC>
 struct Pack {
   uint4 raw;
@@ -191,6 +194,30 @@ struct Pack {
       }
       raw = make_uint4(wd[0], wd[1], wd[2], wd[3]);
     }
+  }
+};
+
+template <>
+struct Pack<__nv_bfloat16, 4> {
+  uint2 raw;
+  __device__ __forceinline__ void zero() { raw = make_uint2(0, 0); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    raw = *reinterpret_cast<const uint2*>(p);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+    *reinterpret_cast<uint2*>(p) = raw;
+  }
+  __device__ __forceinline__ void unpack(float (&f)[4]) const {
+    f[0] = __uint_as_float(raw.x << 16);
+    f[1] = __uint_as_float(raw.x & 0xffff0000u);
+    f[2] = __uint_as_float(raw.y << 16);
+    f[3] = __uint_as_float(raw.y & 0xffff0000u);
+  }
+  __device__ __forceinline__ void pack(const float (&f)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2], f[3]);
+    raw = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                     *reinterpret_cast<const uint32_t*>(&b));
   }
 };
 

@@ -6,8 +6,8 @@
 // A head is read once and written once: the bound is HBM. A group of GL lanes owns a head: each
 // lane holds items of two 16-byte chunks. An item is one rotation pair of chunks (j, j + rot/2)
 // or two neighbouring chunks, so a rotation never leaves its lane; the sum of squares is joined by
-// shuffles. A warp takes one token's heads 32 / GL at a time and walks over tokens, with its
-// weights in registers. The token's angles are worked out once, one per lane, and handed round
+// shuffles. A warp takes one token's heads 32 / GL at a time, the next ones' loads ahead of the
+// arithmetic, and walks over tokens; weights lie in shared memory. The token's angles are worked out once, one per lane, and handed round
 // through shared memory. Angles are reduced in fp64: position * inv_freq in fp32 would be off by
 // 2^-24 of up to 10^5 radians.
 #include "ola_layer.cuh"
@@ -17,28 +17,38 @@ namespace ola {
 namespace {
 
 constexpr int kQkThreads = 128;
+// resident blocks per SM (the launch bounds): the grid is one such wave, each warp walks on
+constexpr int qk_blocks(int ni, int rot) { return ni > 1 ? 4 : rot ? 6 : 8; }
 
 // GL lanes per head, NI items per lane (items past the head's end are idle).
-template <typename T, int GL, int NI, bool PAIR>
-__global__ void __launch_bounds__(kQkThreads) qk_norm_kernel(QkArgs a) {
+// ROT: 0 no rotation, 1 pairs (i, i + rot/2), 2 pairs (2i, 2i + 1).
+template <typename T, int GL, int NI, int ROT>
+__global__ void __launch_bounds__(kQkThreads, qk_blocks(NI, ROT)) qk_norm_kernel(QkArgs a) {
   constexpr int E = 16 / int(sizeof(T));          // elements per chunk
   constexpr int H2 = E / 2;                       // fp32 pairs per chunk
   constexpr int NG = 32 / GL;                     // heads a warp takes together
-  extern __shared__ __align__(16) float sm[];     // per warp: cos and sin of rot / 2 angles
+  extern __shared__ __align__(16) float sm[];     // wq, wk [d] each; per warp: cos, sin
   const int lane = threadIdx.x & 31, gl = lane % GL, grp = lane / GL;
   const int nwarp = gridDim.x * (kQkThreads / 32);
   const int64_t w0 = int64_t(blockIdx.x) * (kQkThreads / 32) + (threadIdx.x >> 5);
-  const int nang = (a.rot / 2 + 31) / 32 * 32;    // table entries, filled up with no rotation
-  float* ct = sm + (threadIdx.x >> 5) * 2 * nang;
+  const int nang = ROT ? (a.rot / 2 + 31) / 32 * 32 : 0;   // table entries, filled up
+  float* ct = sm + 2 * a.d + (threadIdx.x >> 5) * 2 * nang;
   float* st = ct + nang;
   const int nch = a.d / E, half = a.rot / (2 * E), nitem = (nch + 1) / 2;
+  const bool weighted = a.wq || a.wk;
+  if (weighted) {
+    for (int i = threadIdx.x; i < a.d; i += kQkThreads) {
+      sm[i] = a.wq ? __ldg(a.wq + i) : 1.f;
+      sm[a.d + i] = a.wk ? __ldg(a.wk + i) : 1.f;
+    }
+    __syncthreads();
+  }
   // chunks of this lane's items; -1: none
   int c0[NI], c1[NI];
-  uint64_t wq0[NI][H2], wq1[NI][H2], wk0[NI][H2], wk1[NI][H2];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int j = gl + i * GL;
-    if (!PAIR && j < half) {
+    if (ROT == 1 && j < half) {
       c0[i] = j;
       c1[i] = j + half;
     } else {
@@ -47,17 +57,6 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_kernel(QkArgs a) {
     }
     if (j >= nitem) c0[i] = c1[i] = -1;
     if (c1[i] >= nch) c1[i] = -1;
-#pragma unroll
-    for (int e = 0; e < H2; ++e) {
-      auto pair = [&](const float* w, int ch) {
-        return w && ch >= 0 ? f2(__ldg(w + ch * E + 2 * e), __ldg(w + ch * E + 2 * e + 1))
-                            : f2(1.f, 1.f);
-      };
-      wq0[i][e] = pair(a.wq, c0[i]);
-      wq1[i][e] = pair(a.wq, c1[i]);
-      wk0[i][e] = pair(a.wk, c0[i]);
-      wk1[i][e] = pair(a.wk, c1[i]);
-    }
   }
   const int uq = (a.Hq + NG - 1) / NG, uk = (a.Hk + NG - 1) / NG;   // head groups
   const int per = (uq + uk + a.hsplit - 1) / a.hsplit;
@@ -65,7 +64,34 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_kernel(QkArgs a) {
   for (int64_t w = w0; w < a.N * a.hsplit; w += nwarp) {
     const int64_t tok = w / a.hsplit;
     const int part = int(w - tok * a.hsplit);
-    if (a.rot) {
+    const int u0 = part * per, u1 = min(uq + uk, u0 + per);
+    auto head = [&](int u, const T** src, T** dst) -> bool {
+      const bool isq = u < uq;
+      const int h = (isq ? u : u - uq) * NG + grp;
+      *src = (isq ? static_cast<const T*>(a.q) + tok * a.q_tok
+                  : static_cast<const T*>(a.k) + tok * a.k_tok) + int64_t(h) * a.d;
+      *dst = (isq ? static_cast<T*>(a.q_out) + tok * a.qo_tok
+                  : static_cast<T*>(a.k_out) + tok * a.ko_tok) + int64_t(h) * a.d;
+      return u < u1 && h < (isq ? a.Hq : a.Hk);
+    };
+    Pack<T, E> n0[NI], n1[NI];
+    auto fetch = [&](int u) {
+      const T* src;
+      T* dst;
+      const bool on = head(u, &src, &dst);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        n0[i].zero();
+        n1[i].zero();
+        if (on && c0[i] >= 0) n0[i].load(src + c0[i] * E);
+        if (on && c1[i] >= 0) n1[i].load(src + c1[i] * E);
+      }
+    };
+    fetch(u0);
+    // cos, sin of an item's E angles: E pairs of chunks (j, j + half), or E / 2 pairs inside each
+    // of the two chunks; item j holds the angles j E .. j E + E - 1 in both
+    uint64_t cs[NI][H2], sn[NI][H2];
+    if (ROT) {
       __syncwarp();
       const double pos = double(__ldg(a.pos + tok));
       for (int f = lane; f < nang; f += 32) {
@@ -79,11 +105,6 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_kernel(QkArgs a) {
         st[f] = s;
       }
       __syncwarp();
-    }
-    // cos, sin of an item's E angles: E pairs of chunks (j, j + half), or E / 2 pairs inside each
-    // of the two chunks; item j holds the angles j E .. j E + E - 1 in both
-    uint64_t cs[NI][H2], sn[NI][H2];
-    if (a.rot) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int f = (gl + i * GL) * E;
@@ -101,29 +122,17 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_kernel(QkArgs a) {
         }
       }
     }
-    const int u1 = min(uq + uk, (part + 1) * per);
-    for (int u = part * per; u < u1; ++u) {
-      const bool isq = u < uq;
-      const int h = (isq ? u : u - uq) * NG + grp;
-      const bool on = h < (isq ? a.Hq : a.Hk);
-      const T* src = (isq ? static_cast<const T*>(a.q) + tok * a.q_tok
-                          : static_cast<const T*>(a.k) + tok * a.k_tok) + int64_t(h) * a.d;
-      T* dst = (isq ? static_cast<T*>(a.q_out) + tok * a.qo_tok
-                    : static_cast<T*>(a.k_out) + tok * a.ko_tok) + int64_t(h) * a.d;
-      Pack<T, E> r0[NI], r1[NI];
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        r0[i].zero();
-        r1[i].zero();
-        if (on && c0[i] >= 0) r0[i].load(src + c0[i] * E);
-        if (on && c1[i] >= 0) r1[i].load(src + c1[i] * E);
-      }
+#pragma unroll 1
+    for (int u = u0; u < u1; ++u) {
+      const T* src;
+      T* dst;
+      const bool on = head(u, &src, &dst);
       uint64_t x0[NI][H2], x1[NI][H2], s2 = f2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         float f0[E], f1[E];
-        r0[i].unpack(f0);
-        r1[i].unpack(f1);
+        n0[i].unpack(f0);
+        n1[i].unpack(f1);
 #pragma unroll
         for (int e = 0; e < H2; ++e) {
           x0[i][e] = f2(f0[2 * e], f0[2 * e + 1]);
@@ -131,6 +140,7 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_kernel(QkArgs a) {
           s2 = fma2(x0[i][e], x0[i][e], fma2(x1[i][e], x1[i][e], s2));
         }
       }
+      fetch(u + 1);
       const float2 st2 = un2(s2);
       float s = st2.x + st2.y;
 #pragma unroll
@@ -138,15 +148,28 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_kernel(QkArgs a) {
       const float rs = rsqrtf((a.l2 ? s : s * inv_d) + a.eps);
       if (!on) continue;
       const uint64_t rs2 = f2(rs, rs);
+      const float* wt = sm + (u < uq ? 0 : a.d);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         if (c0[i] < 0) continue;
+        const int d1 = c1[i] < 0 ? c0[i] : c1[i];
 #pragma unroll
         for (int e = 0; e < H2; ++e) {
-          x0[i][e] = mul2(mul2(x0[i][e], rs2), isq ? wq0[i][e] : wk0[i][e]);
-          x1[i][e] = mul2(mul2(x1[i][e], rs2), isq ? wq1[i][e] : wk1[i][e]);
+          x0[i][e] = mul2(x0[i][e], rs2);
+          x1[i][e] = mul2(x1[i][e], rs2);
         }
-        if (!PAIR) {
+        if (weighted) {
+#pragma unroll
+          for (int e = 0; e < H2; e += 2) {
+            const ulonglong2 a2 = *reinterpret_cast<const ulonglong2*>(wt + c0[i] * E + 2 * e);
+            const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(wt + d1 * E + 2 * e);
+            x0[i][e] = mul2(x0[i][e], a2.x);
+            x0[i][e + 1] = mul2(x0[i][e + 1], a2.y);
+            x1[i][e] = mul2(x1[i][e], b2.x);
+            x1[i][e + 1] = mul2(x1[i][e + 1], b2.y);
+          }
+        }
+        if (ROT == 1) {
           if (c0[i] < half) {
             const uint64_t neg = f2(-1.f, -1.f);
 #pragma unroll
@@ -156,9 +179,9 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_kernel(QkArgs a) {
               x1[i][e] = fma2(q, cs[i][e], mul2(p, sn[i][e]));
             }
           }
-        } else if (c0[i] * E < a.rot) {
+        } else if (ROT == 2) {
           // rot is a multiple of 16, so a chunk is rotated as a whole or not at all
-          const bool both = c1[i] * E < a.rot;
+          const bool one = c0[i] * E < a.rot, both = c1[i] * E < a.rot;
 #pragma unroll
           for (int e = 0; e < H2; ++e) {
             // pair e of chunk 0 has angle e, of chunk 1 angle E / 2 + e
@@ -167,8 +190,8 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_kernel(QkArgs a) {
               const float c = k & 1 ? c2.y : c2.x, t = k & 1 ? t2.y : t2.x;
               return f2(xy.x * c - xy.y * t, xy.y * c + xy.x * t);
             };
-            x0[i][e] = turn(x0[i][e], e);
-            if (both) x1[i][e] = turn(x1[i][e], H2 + e);
+            if (one) x0[i][e] = turn(x0[i][e], e);
+            if (one && both) x1[i][e] = turn(x1[i][e], H2 + e);
           }
         }
         float f[E];
@@ -198,11 +221,14 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_kernel(QkArgs a) {
 
 template <typename T, int GL, int NI>
 cudaError_t run(const QkArgs& a, int pair, unsigned grid, cudaStream_t st) {
-  const size_t smem = sizeof(float) * 2 * ((a.rot / 2 + 31) / 32 * 32) * (kQkThreads / 32);
-  if (pair)
-    qk_norm_kernel<T, GL, NI, true><<<grid, kQkThreads, smem, st>>>(a);
+  const int nang = a.rot ? (a.rot / 2 + 31) / 32 * 32 : 0;
+  const size_t smem = sizeof(float) * 2 * (a.d + nang * (kQkThreads / 32));
+  if (!a.rot)
+    qk_norm_kernel<T, GL, NI, 0><<<grid, kQkThreads, smem, st>>>(a);
+  else if (pair)
+    qk_norm_kernel<T, GL, NI, 2><<<grid, kQkThreads, smem, st>>>(a);
   else
-    qk_norm_kernel<T, GL, NI, false><<<grid, kQkThreads, smem, st>>>(a);
+    qk_norm_kernel<T, GL, NI, 1><<<grid, kQkThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -221,9 +247,9 @@ cudaError_t launch_qk_norm(QkArgs a, int in_dtype, int pair, cudaStream_t st) {
   const int groups = (a.Hq + ng - 1) / ng + (a.Hk + ng - 1) / ng;
   a.hsplit = 1;
   while (a.hsplit < groups && a.N * a.hsplit < int64_t(16) * sms) a.hsplit *= 2;
-  // enough blocks to fill the machine; each warp walks on from token to token
   int64_t grid = (a.N * a.hsplit * 32 + kQkThreads - 1) / kQkThreads;
-  if (grid > int64_t(sms) * 8) grid = int64_t(sms) * 8;
+  const int64_t most = int64_t(sms) * qk_blocks(nitem > 32 ? 2 : 1, a.rot);
+  if (grid > most) grid = most;
   const unsigned g = unsigned(grid);
   if (in_dtype == OLA_BF16) {
     if (gl == 1) return run<__nv_bfloat16, 1, 1>(a, pair, g, st);
