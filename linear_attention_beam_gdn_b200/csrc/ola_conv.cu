@@ -9,6 +9,8 @@
 // in once, transposed through shared memory ([tap][channel], read 16 bytes at a time); sums run two
 // channels per instruction. The window's values are moved, never recomputed: the state that leaves
 // is the input's bits.
+#include <type_traits>
+
 #include "ola_layer.cuh"
 
 namespace ola {
@@ -85,7 +87,7 @@ struct Taps {
     }
   }
   // win[0..W-2] the earlier tokens, oldest first, x the newest
-  __device__ __forceinline__ void apply(const Pairs<T, VEC> (&win)[W - 1], const Pairs<T, VEC>& x,
+  __device__ __forceinline__ void apply(const Pairs<T, VEC>* win, const Pairs<T, VEC>& x,
                                         int silu, Pairs<T, VEC>& y) const {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
@@ -117,20 +119,30 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvArgs a) {
   // 16-byte vectors come through a ring of kAhead groups of tokens in shared memory, which every
   // thread fills for itself: deep prefetch without registers and without barriers
   constexpr bool ASYNC = VEC * sizeof(T) == 16;
-  T* ring = reinterpret_cast<T*>(sm + (W + 1) * nc) +
-            size_t(threadIdx.y * blockDim.x + threadIdx.x) * VEC;
-  auto fetch_async = [&](int t, int slot) {
+  constexpr int kVecBytes = VEC * int(sizeof(T)), kSlot = kConvThreads * kVecBytes;
+  unsigned char* ring = reinterpret_cast<unsigned char*>(sm + (W + 1) * nc) +
+                        (threadIdx.y * blockDim.x + threadIdx.x) * kVecBytes;
+  const int64_t xs = a.x_tok * int64_t(sizeof(T)), ys = a.y_tok * int64_t(sizeof(T));
+  const char* xl = reinterpret_cast<const char*>(x + int64_t(t0) * a.x_tok);   // next to load
+  int tl = t0, sl = 0;                                       // its token, its slot
+  auto fetch_async = [&]() {
     if constexpr (ASYNC) {
+      unsigned char* dst = ring + sl * (kConvUnroll * kSlot);
+      if (tl + kConvUnroll <= t1) {
 #pragma unroll
-      for (int i = 0; i < kConvUnroll; ++i)
-        if (t + i < t1)
-          cp_async16(ring + size_t(slot * kConvUnroll + i) * kConvThreads * VEC,
-                     x + int64_t(t + i) * a.x_tok);
+        for (int i = 0; i < kConvUnroll; ++i, xl += xs) cp_async16(dst + i * kSlot, xl);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kConvUnroll; ++i, xl += xs)
+          if (tl + i < t1) cp_async16(dst + i * kSlot, xl);
+      }
+      tl += kConvUnroll;
+      sl = sl + 1 < kAhead ? sl + 1 : 0;
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
   };
 #pragma unroll
-  for (int s = 0; s < kAhead; ++s) fetch_async(t0 + s * kConvUnroll, s);
+  for (int s = 0; s < kAhead; ++s) fetch_async();
   Taps<T, VEC, W> taps;
   taps.load(a, sm, c0, nc, cl);
   if (!active) return;
@@ -177,34 +189,45 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvArgs a) {
     }
   }
   int slot = 0;
-  for (int t = t0; t < t1; t += kConvUnroll) {
+  char* yl = reinterpret_cast<char*>(y + int64_t(t0) * a.y_tok);
+  const char* xr = reinterpret_cast<const char*>(x + int64_t(t0) * a.x_tok);
+  // kConvUnroll tokens from registers; ALL: every one of them exists
+  auto group = [&](auto all, int t) {
+    constexpr bool ALL = decltype(all)::value;
     Pack<T, VEC> in[kConvUnroll];
     if constexpr (ASYNC) asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
 #pragma unroll
     for (int i = 0; i < kConvUnroll; ++i) {
       if constexpr (ASYNC) {
-        in[i].load(ring + size_t(slot * kConvUnroll + i) * kConvThreads * VEC);
+        in[i].load(reinterpret_cast<const T*>(ring + (slot * kConvUnroll + i) * kSlot));
       } else {
         in[i].zero();
-        if (t + i < t1) in[i].load(x + int64_t(t + i) * a.x_tok);
+        if (ALL || t + i < t1) in[i].load(reinterpret_cast<const T*>(xr));
+        xr += xs;
       }
     }
-    fetch_async(t + kAhead * kConvUnroll, slot);
     slot = slot + 1 < kAhead ? slot + 1 : 0;
+    fetch_async();
+    Pairs<T, VEC> u[W - 1 + kConvUnroll];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) u[j] = win[j];
 #pragma unroll
     for (int i = 0; i < kConvUnroll; ++i) {
-      if (t + i >= t1) break;
-      Pairs<T, VEC> xf, yf;
-      xf.from(in[i]);
-      taps.apply(win, xf, a.silu, yf);
+      u[W - 1 + i].from(in[i]);
+      Pairs<T, VEC> yf;
+      taps.apply(u + i, u[W - 1 + i], a.silu, yf);
       Pack<T, VEC> o;
       yf.to(o);
-      o.store(y + int64_t(t + i) * a.y_tok);
-#pragma unroll
-      for (int j = 0; j < W - 2; ++j) win[j] = win[j + 1];
-      win[W - 2] = xf;
+      if (ALL || t + i < t1) o.store(reinterpret_cast<T*>(yl));
+      yl += ys;
     }
-  }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) win[j] = u[kConvUnroll + j];
+  };
+  int t = t0;
+#pragma unroll 1
+  for (; t + kConvUnroll <= t1; t += kConvUnroll) group(std::true_type{}, t);
+  if (t < t1) group(std::false_type{}, t);
 }
 
 // One token of every beam: thread = 16 bytes of channels x tt consecutive beams (of all requests).

@@ -65,20 +65,19 @@ __global__ void __launch_bounds__(kQkThreads, qk_blocks(NI, ROT)) qk_norm_kernel
     const int64_t tok = w / a.hsplit;
     const int part = int(w - tok * a.hsplit);
     const int u0 = part * per, u1 = min(uq + uk, u0 + per);
-    auto head = [&](int u, const T** src, T** dst) -> bool {
-      const bool isq = u < uq;
-      const int h = (isq ? u : u - uq) * NG + grp;
-      *src = (isq ? static_cast<const T*>(a.q) + tok * a.q_tok
-                  : static_cast<const T*>(a.k) + tok * a.k_tok) + int64_t(h) * a.d;
-      *dst = (isq ? static_cast<T*>(a.q_out) + tok * a.qo_tok
-                  : static_cast<T*>(a.k_out) + tok * a.ko_tok) + int64_t(h) * a.d;
-      return u < u1 && h < (isq ? a.Hq : a.Hk);
-    };
+    // this lane group's head in q's and k's rows, and the step to the next one
+    const int64_t step = int64_t(NG) * a.d;
+    const T* qs = static_cast<const T*>(a.q) + tok * a.q_tok + (int64_t(u0) * NG + grp) * a.d;
+    T* qd = static_cast<T*>(a.q_out) + tok * a.qo_tok + (int64_t(u0) * NG + grp) * a.d;
+    const int uk0 = u0 > uq ? u0 - uq : 0;
+    const T* ks = static_cast<const T*>(a.k) + tok * a.k_tok + (int64_t(uk0) * NG + grp) * a.d;
+    T* kd = static_cast<T*>(a.k_out) + tok * a.ko_tok + (int64_t(uk0) * NG + grp) * a.d;
     Pack<T, E> n0[NI], n1[NI];
-    auto fetch = [&](int u) {
-      const T* src;
-      T* dst;
-      const bool on = head(u, &src, &dst);
+    auto fetch = [&](int u) {                     // called for u0, u0 + 1, ... in turn
+      const bool isq = u < uq;
+      const T* src = isq ? qs : ks;
+      const bool on = u < u1 && (isq ? u * NG + grp < a.Hq : (u - uq) * NG + grp < a.Hk);
+      if (isq) qs += step; else ks += step;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         n0[i].zero();
@@ -124,9 +123,10 @@ __global__ void __launch_bounds__(kQkThreads, qk_blocks(NI, ROT)) qk_norm_kernel
     }
 #pragma unroll 1
     for (int u = u0; u < u1; ++u) {
-      const T* src;
-      T* dst;
-      const bool on = head(u, &src, &dst);
+      const bool isq = u < uq;
+      const bool on = isq ? u * NG + grp < a.Hq : (u - uq) * NG + grp < a.Hk;
+      T* dst = isq ? qd : kd;
+      if (isq) qd += step; else kd += step;
       uint64_t x0[NI][H2], x1[NI][H2], s2 = f2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kQkThreads, qk_blocks(NI, ROT)) qk_norm_kernel
       const float rs = rsqrtf((a.l2 ? s : s * inv_d) + a.eps);
       if (!on) continue;
       const uint64_t rs2 = f2(rs, rs);
-      const float* wt = sm + (u < uq ? 0 : a.d);
+      const float* wt = sm + (isq ? 0 : a.d);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         if (c0[i] < 0) continue;
