@@ -324,11 +324,12 @@ cudaError_t launch(ConvArgs a, int in_dtype, int W, bool wide, bool step, cudaSt
   const int64_t seqs = step ? 1 : a.R;
   a.tt = step ? 16 : 32;
   const int least = step ? 2 : 4;
+  const int64_t least_blocks = int64_t(step || !wide ? 8 : 1) * sms;
   auto blocks = [&](int tt) {
     const int64_t n = (rows + int64_t(tt) * by - 1) / (int64_t(tt) * by);
     return (n < 1 ? 1 : n) * seqs * a.n_ctile;
   };
-  while (a.tt > least && blocks(a.tt) < int64_t(8) * sms) a.tt /= 2;
+  while (a.tt > least && blocks(a.tt) < least_blocks) a.tt /= 2;
   const int64_t grid = blocks(a.tt);
   a.n_ttile = int(grid / seqs / a.n_ctile);
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;

@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   uint64_t* kq_full = bar;               // [NST] keys and queries landed (TMA bytes)
   uint64_t* kq_free = bar + NST;         // [NST] ... read by the products (one commit per issuer)
   uint64_t* v_full = bar + 2 * NST;      // [NST] values landed (TMA bytes)
-  uint64_t* v_done = bar + 3 * NST;      // [NST] y written over them (8 warps); dS done if !FULL
+  uint64_t* v_done = bar + 3 * NST;      // [NST] values read (commit, 4 W V and 8 output warps); dS done if !FULL
   uint64_t* sc_full = bar + 4 * NST;     // [NST] scalars written (4 warps)
   uint64_t* sc_free = bar + 5 * NST;     // [NST] scalars read (commits, state and output warps)
   uint64_t* x_done = bar + 6 * NST;      // [NST] values read by the W V warps (4 warps)
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       mbar_init(&kq_full[s], 1);
       mbar_init(&kq_free[s], FULL ? 2 : 1);
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_done[s], FULL ? 8 : 1);
+      mbar_init(&v_done[s], FULL ? 13 : 1);
       mbar_init(&sc_full[s], 4);
       mbar_init(&sc_free[s], FULL ? 14 : 5);
       mbar_init(&x_done[s], 4);
@@ -311,6 +311,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
                 umma_bf16(tmem + kTY2, dq + (k >> 2) * (kBlk >> 4) + (k & 3) * 2, dsd + k * 128,
                           id_y, k != 0);
               umma_commit(y_full);
+              umma_commit(&v_done[s]);
               umma_commit(&kq_free[s]);
               umma_commit(&sc_free[s]);
             }
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       mbar_wait_bounded(done, 0);              // both issuers, before tensor memory is released
       __syncwarp();
     } else if (warp == 26) {
-      // ---------------------------------------------------------------- values in, y out
+      // ---------------------------------------------------------------- values
       if (lane == 0) {
         prefetch_tmap(&c.mv);
         auto load = [&](int i) {
@@ -340,18 +341,10 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
             report_error(a.err, OLA_ERR_TIMEOUT, 66, i);
             break;
           }
-          // rows past P are clipped; a sequence that ends inside the chunk but before P was
-          // stored row by row
-          if (FULL && (p0 + (i + 1) * kQ <= p1 || p1 == a.P)) {
-            tma_store_4d(&c.my, sm + Y::kV + s * kBlk, kNV * tile, h, p0 + i * kQ, r);
-            bulk_commit();
-            bulk_wait_read();
-          }
           if (issued < nch) load(issued++);
         }
         for (int i = issued > NST ? issued - NST : 0; i < issued; ++i)
           mbar_wait_bounded(&v_full[i % NST], (i / NST) & 1);
-        bulk_wait_all();
       }
       __syncwarp();
     } else {
@@ -558,6 +551,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       if (lane == 0) {
         mbar_arrive(&xw_full[w4 >> 1]);
         mbar_arrive(&x_done[s]);
+        if (FULL) mbar_arrive(&v_done[s]);
       }
     }
     if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 63, 0);
@@ -693,8 +687,8 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         const uint64_t ec2 = f2(ec, ec);
         warp_arrive(&sc_free[s]);
         unsigned char* vrow = sm + Y::kV + s * kBlk + t * 128;
-        const bool by_tma = p0 + (i + 1) * kQ <= p1 || p1 == a.P;
-        ok = warp_wait(y_full, i) && warp_wait(&x_done[s], i / NST);
+        if (!skip) warp_arrive(&v_done[s]);
+        ok = warp_wait(y_full, i);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
@@ -733,16 +727,13 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
               ow[e] = pack2(o[e]);
             }
             const uint4 o4 = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-            if (by_tma)
-              *reinterpret_cast<uint4*>(at[u]) = o4;
-            else if (live && 8 * (2 * hq + u) < nv)
+            if (live && 8 * (2 * hq + u) < nv)
               *(reinterpret_cast<uint4*>(yp + int64_t(p) * a.y_tok) + 2 * hq + u) = o4;
           }
         }
         tc_fence_before();
         warp_arrive(y_free);
-        fence_proxy_async_smem();
-        warp_arrive(&v_done[s]);
+        if (skip) warp_arrive(&v_done[s]);
       }
       if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 65, 0);
     }
