@@ -20,13 +20,13 @@
 // One block per (sequence, head, 64 value columns, piece), one per SM:
 //   warps 0-7    G -> P (thread = token t, half of the columns; P into tensor memory as the A
 //                operand of Y1); warps 0-3 also the next chunk's scalars (dt, running sums)
-//   warps 8-15   outputs (thread = token t, half of the columns): Y1 + e^{c_t} Y2, D, gate; y staged
-//                over v
+//   warps 8-15   outputs (thread = token t, half of the columns): Y1 + e^{c_t} Y2, D, gate; y
+//                stored from registers
 //   warps 16-19  W V (thread = token s)
 //   warps 20-23  state rows (thread = key column, S^T in tensor memory): S = e^{c_C} S + dS and its
 //                bf16 copy
 //   warp 24      tcgen05.mma: dS;   warp 25  tcgen05.mma: Y1, the next chunk's G, Y2
-//   warp 26      TMA stores of y and loads of v
+//   warp 26      TMA loads of v
 //   warp 27      TMA loads of keys and queries
 // Two issuing warps, so that neither chain (G -> P -> Y1 and W V -> dS -> S -> Y2) waits behind the
 // other's operands; nothing but Y2 waits for the state. A piece of a cut sequence runs twice: dS alone first (FULL = false), then, once
@@ -45,7 +45,7 @@ constexpr uint32_t kBlk = kQ * 128;     // 16 KB: 128 rows of 64 bf16 columns
 // tensor memory columns
 constexpr uint32_t kTG = 0;             // G, 128
 constexpr uint32_t kTP = 128;           // P as bf16 pairs, 64
-constexpr uint32_t kTD = 192;           // dS: first part of W V, then the two others, 64 each
+constexpr uint32_t kTD = 192;           // dS, two buffers of 64
 constexpr uint32_t kTS = 320;           // S^T fp32, 64
 constexpr uint32_t kTY1 = 384;
 constexpr uint32_t kTY2 = 448;
@@ -62,7 +62,7 @@ struct Lay {
   static constexpr uint32_t kS = kXw + 3 * kBlk;           // state copy [64 KB rows][64 columns]
   static constexpr uint32_t kSc = kS + KB * 8192;          // scalars per stage
   static constexpr uint32_t kBar = kSc + NST * kScFloats * 4;
-  static constexpr int kNBar = 7 * NST + 11;
+  static constexpr int kNBar = 6 * NST + 13;
   static constexpr uint32_t kBytes = kBar + kNBar * 8 + 16;
 };
 static_assert(Lay<1>::kBar % 8 == 0 && Lay<2>::kBar % 8 == 0, "mbarriers");
@@ -70,7 +70,7 @@ static_assert(Lay<1>::kBytes <= 232448 && Lay<2>::kBytes <= 232448, "shared memo
 static_assert((kScFloats * 4) % 16 == 0, "float4 rows of scalars");
 
 struct ChunkScan {
-  CUtensorMap mv, mk, mq, my;           // [R][P][heads][d] bf16, boxes of 64 x 1 x 128 x 1
+  CUtensorMap mv, mk, mq;               // [R][P][heads][d] bf16, boxes of 64 x 1 x 128 x 1
   ScanArgs a;
   int ntile;                            // blocks of 64 value columns
 };
@@ -79,8 +79,6 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 __device__ __forceinline__ uint32_t pack2(uint64_t a) {
   const float2 f = un2(a);
@@ -116,23 +114,6 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0;
 }
 
-__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int c0,
-                                             int c1, int c2, int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::
-          "l"(reinterpret_cast<uint64_t>(map)),
-      "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
-__device__ __forceinline__ void bulk_commit() {
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-__device__ __forceinline__ void bulk_wait_all() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase) {
   return __all_sync(kFull, mbar_wait_bounded(bar, uint32_t(phase) & 1u));
@@ -154,17 +135,17 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   uint64_t* v_done = bar + 3 * NST;      // [NST] values read (commit, 4 W V and 8 output warps); dS done if !FULL
   uint64_t* sc_full = bar + 4 * NST;     // [NST] scalars written (4 warps)
   uint64_t* sc_free = bar + 5 * NST;     // [NST] scalars read (commits, state and output warps)
-  uint64_t* x_done = bar + 6 * NST;      // [NST] values read by the W V warps (4 warps)
-  uint64_t* one = bar + 7 * NST;
+  uint64_t* one = bar + 6 * NST;
   uint64_t* xw_full = one + 0;           // [2] W V of 64 tokens written (2 warps)
   uint64_t* xw_free = one + 2;           // [2] ... read by dS (commit)
   uint64_t* ds_full = one + 4;           // dS done
   uint64_t* g_full = one + 5;            // G done, and Y1 of the chunk before
   uint64_t* p_full = one + 6;            // G read and P written (8 warps)
-  uint64_t* s_full = one + 7;            // dS read, state and its copy written (4 warps)
+  uint64_t* s_full = one + 7;            // state copy written (4 warps)
   uint64_t* y_full = one + 8;            // Y1 and Y2 done
   uint64_t* y_free = one + 9;            // Y1 and Y2 read (8 warps)
-  uint64_t* done = one + 10;             // every MMA completed (both issuers)
+  uint64_t* ds_free = one + 10;          // [2] dS buffer read (4 warps)
+  uint64_t* done = one + 12;             // every MMA completed (both issuers)
   uint32_t* holder = reinterpret_cast<uint32_t*>(bar + Y::kNBar);
   const ScanArgs& a = c.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -192,11 +173,11 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       mbar_init(&v_done[s], FULL ? 13 : 1);
       mbar_init(&sc_full[s], 4);
       mbar_init(&sc_free[s], FULL ? 14 : 5);
-      mbar_init(&x_done[s], 4);
     }
     for (int u = 0; u < 2; ++u) {
       mbar_init(&xw_full[u], 2);
       mbar_init(&xw_free[u], 1);
+      mbar_init(&ds_free[u], 4);
     }
     mbar_init(ds_full, 1);
     mbar_init(g_full, 1);
@@ -219,14 +200,14 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
     if (warp == 24) {
       // ---------------------------------------------------------------- product dS
       // A = keys read MN-major (key columns along M; for d_k <= 64 the upper 64 rows read the next
-      // tile and are not used), B = the first two parts of W V side by side; the third is added to
-      // the second
-      const uint32_t id_d2 = idesc_bf16_f32_amn(128, 2 * kNV) | (1u << 16);      // A, B MN-major
-      const uint32_t id_d1 = idesc_bf16_f32_amn(128, kNV) | (1u << 16);
+      // tile and are not used), B = the three parts of W V one after the other; two buffers
+      const uint32_t id_d = idesc_bf16_f32_amn(128, kNV) | (1u << 16);           // A, B MN-major
       bool ok = true;
       for (int i = 0; i < nch; ++i) {
         const int s = i % NST;
-        ok = warp_wait(&kq_full[s], i / NST) && warp_wait(s_full, i);
+        const uint32_t dst = tmem + kTD + kNV * (i & 1);
+        ok = warp_wait(&kq_full[s], i / NST) &&
+             (i < 2 || warp_wait(&ds_free[i & 1], (i >> 1) - 1));
 #pragma unroll 1
         for (int u = 0; u < 2 && ok; ++u) {              // 64 tokens each
           ok = warp_wait(&xw_full[u], i);
@@ -237,8 +218,10 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
             const uint64_t dx = sw128_mnmajor_desc(base + Y::kXw + u * 8192, kBlk, 1024);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              umma_bf16(tmem + kTD, dk + k * 128, dx + k * 128, id_d2, k != 0 || u != 0);
-              umma_bf16(tmem + kTD + kNV, dk + k * 128, dx + (2 * kBlk >> 4) + k * 128, id_d1, 1u);
+#pragma unroll
+              for (int part = 0; part < 3; ++part)
+                umma_bf16(dst, dk + k * 128, dx + part * (kBlk >> 4) + k * 128, id_d,
+                          u != 0 || k != 0 || part != 0);
             }
             umma_commit(&xw_free[u]);
             if (u == 1) {
@@ -269,7 +252,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
             ok = warp_wait(p_full, i) && warp_wait(&v_full[s], i / NST) &&
                  (i == 0 || warp_wait(y_free, i - 1));
             // (the values' rows behind the end of a padded sequence are cleared by then)
-            if (ok && p1 - (p0 + i * kQ) < kQ) ok = warp_wait(&x_done[s], i / NST);
+            if (ok && p1 - (p0 + i * kQ) < kQ) ok = warp_wait(&xw_full[0], i) && warp_wait(&xw_full[1], i);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
@@ -550,7 +533,6 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&xw_full[w4 >> 1]);
-        mbar_arrive(&x_done[s]);
         if (FULL) mbar_arrive(&v_done[s]);
       }
     }
@@ -610,17 +592,20 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       tc_fence_after();
 #pragma unroll 1
       for (int q = 0; q < 8; q += 2) {
-        float d[48];
-        tmem_ld16x3(tl + kTD + 8 * q, tl + kTD + kNV + 8 * q, tl + kTS + 8 * q, d);
+        uint32_t d[16], old16[16];
+        tmem_ld16x2(tl + kTD + kNV * (i & 1) + 8 * q, tl + kTS + 8 * q, d, old16);
+        if (q == 6) {
+          tc_fence_before();
+          warp_arrive(&ds_free[i & 1]);
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           uint32_t x[8];
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
             const int b = 8 * u + e;
-            const uint64_t old = f2(d[32 + b], d[33 + b]);
-            const float2 n2 = un2(fma2(
-                mul, old, fma2(keep, old, add2(f2(d[b], d[b + 1]), f2(d[16 + b], d[17 + b])))));
+            const uint64_t old = u2(old16[b], old16[b + 1]);
+            const float2 n2 = un2(fma2(mul, old, fma2(keep, old, u2(d[b], d[b + 1]))));
             x[e] = __float_as_uint(n2.x);
             x[e + 1] = __float_as_uint(n2.y);
           }
@@ -770,8 +755,7 @@ EncodeFn map_encoder() {
 }
 
 // [R][P][heads][d] bf16 with the given strides as a 4-D map (column, head, token, sequence) of
-// 64 x 1 x 128 x 1 boxes, 128-byte swizzle. Columns past d and tokens past P read 0 and are not
-// written.
+// 64 x 1 x 128 x 1 boxes, 128-byte swizzle. Columns past d and tokens past P read 0.
 bool rows_map(CUtensorMap* map, const void* base, int d, int heads, int P, int R, int64_t tok,
               int64_t seq) {
   EncodeFn fn = map_encoder();
@@ -846,8 +830,7 @@ cudaError_t launch_scan_chunk(const ScanArgs& a, cudaStream_t st) {
   c.ntile = (a.d_v + kNV - 1) / kNV;
   if (!rows_map(&c.mv, a.v, a.d_v, a.H, a.P, a.R, a.v_tok, a.v_seq) ||
       !rows_map(&c.mk, a.k, a.d_k, a.G, a.P, a.R, a.k_tok, a.k_seq) ||
-      !rows_map(&c.mq, a.q, a.d_k, a.G, a.P, a.R, a.q_tok, a.q_seq) ||
-      !rows_map(&c.my, a.y, a.d_v, a.H, a.P, a.R, a.y_tok, a.y_seq))
+      !rows_map(&c.mq, a.q, a.d_k, a.G, a.P, a.R, a.q_tok, a.q_seq))
     return cudaErrorInvalidValue;
   return a.d_k <= 64 ? run<1>(c, st) : run<2>(c, st);
 }
