@@ -22,12 +22,12 @@
 //                operand of Y1); warps 0-3 also the next chunk's scalars (dt, running sums)
 //   warps 8-15   outputs (thread = token t, half of the columns): Y1 + e^{c_t} Y2, D, gate; y
 //                stored from registers
-//   warps 16-19  W V (thread = token s)
-//   warps 20-23  state rows (thread = key column, S^T in tensor memory): S = e^{c_C} S + dS and its
+//   warps 16-23  W V (thread = token s, half of the columns)
+//   warps 24-27  state rows (thread = key column, S^T in tensor memory): S = e^{c_C} S + dS and its
 //                bf16 copy
-//   warp 24      tcgen05.mma: dS;   warp 25  tcgen05.mma: Y1, the next chunk's G, Y2
-//   warp 26      TMA loads of v
-//   warp 27      TMA loads of keys and queries
+//   warp 28      tcgen05.mma: dS;   warp 29  tcgen05.mma: Y1, the next chunk's G, Y2
+//   warp 30      TMA loads of v
+//   warp 31      TMA loads of keys and queries
 // Two issuing warps, so that neither chain (G -> P -> Y1 and W V -> dS -> S -> Y2) waits behind the
 // other's operands; nothing but Y2 waits for the state. A piece of a cut sequence runs twice: dS alone first (FULL = false), then, once
 // scan_join_kernel has made the state before every piece, the outputs.
@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kQ = 128;                 // tokens per chunk
 constexpr int kNV = 64;                 // value columns per block
-constexpr int kThr = 896;
+constexpr int kThr = 1024;
 constexpr uint32_t kBlk = kQ * 128;     // 16 KB: 128 rows of 64 bf16 columns
 
 // tensor memory columns
@@ -62,7 +62,7 @@ struct Lay {
   static constexpr uint32_t kS = kXw + 3 * kBlk;           // state copy [64 KB rows][64 columns]
   static constexpr uint32_t kSc = kS + KB * 8192;          // scalars per stage
   static constexpr uint32_t kBar = kSc + NST * kScFloats * 4;
-  static constexpr int kNBar = 6 * NST + 13;
+  static constexpr int kNBar = 6 * NST + 14;
   static constexpr uint32_t kBytes = kBar + kNBar * 8 + 16;
 };
 static_assert(Lay<1>::kBar % 8 == 0 && Lay<2>::kBar % 8 == 0, "mbarriers");
@@ -132,20 +132,21 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   uint64_t* kq_full = bar;               // [NST] keys and queries landed (TMA bytes)
   uint64_t* kq_free = bar + NST;         // [NST] ... read by the products (one commit per issuer)
   uint64_t* v_full = bar + 2 * NST;      // [NST] values landed (TMA bytes)
-  uint64_t* v_done = bar + 3 * NST;      // [NST] values read (commit, 4 W V and 8 output warps); dS done if !FULL
+  uint64_t* v_done = bar + 3 * NST;      // [NST] values read (commit, 8 W V and 8 output warps); dS done if !FULL
   uint64_t* sc_full = bar + 4 * NST;     // [NST] scalars written (4 warps)
   uint64_t* sc_free = bar + 5 * NST;     // [NST] scalars read (commits, state and output warps)
   uint64_t* one = bar + 6 * NST;
-  uint64_t* xw_full = one + 0;           // [2] W V of 64 tokens written (2 warps)
+  uint64_t* xw_full = one + 0;           // [2] W V of 64 tokens written (4 warps)
   uint64_t* xw_free = one + 2;           // [2] ... read by dS (commit)
-  uint64_t* ds_full = one + 4;           // dS done
-  uint64_t* g_full = one + 5;            // G done, and Y1 of the chunk before
-  uint64_t* p_full = one + 6;            // G read and P written (8 warps)
-  uint64_t* s_full = one + 7;            // state copy written (4 warps)
-  uint64_t* y_full = one + 8;            // Y1 and Y2 done
-  uint64_t* y_free = one + 9;            // Y1 and Y2 read (8 warps)
-  uint64_t* ds_free = one + 10;          // [2] dS buffer read (4 warps)
-  uint64_t* done = one + 12;             // every MMA completed (both issuers)
+  uint64_t* ds_full = one + 4;           // [2] dS buffer done; one barrier per buffer: a state warp
+                                         // may be a chunk behind the product
+  uint64_t* ds_free = one + 6;           // [2] dS buffer read (4 warps)
+  uint64_t* g_full = one + 8;            // G done, and Y1 of the chunk before
+  uint64_t* p_full = one + 9;            // G read and P written (8 warps)
+  uint64_t* s_full = one + 10;           // state copy written (4 warps)
+  uint64_t* y_full = one + 11;           // Y1 and Y2 done
+  uint64_t* y_free = one + 12;           // Y1 and Y2 read (8 warps)
+  uint64_t* done = one + 13;             // every MMA completed (both issuers)
   uint32_t* holder = reinterpret_cast<uint32_t*>(bar + Y::kNBar);
   const ScanArgs& a = c.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -170,16 +171,16 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       mbar_init(&kq_full[s], 1);
       mbar_init(&kq_free[s], FULL ? 2 : 1);
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_done[s], FULL ? 13 : 1);
+      mbar_init(&v_done[s], FULL ? 17 : 1);
       mbar_init(&sc_full[s], 4);
       mbar_init(&sc_free[s], FULL ? 14 : 5);
     }
     for (int u = 0; u < 2; ++u) {
-      mbar_init(&xw_full[u], 2);
+      mbar_init(&xw_full[u], 4);
       mbar_init(&xw_free[u], 1);
+      mbar_init(&ds_full[u], 1);
       mbar_init(&ds_free[u], 4);
     }
-    mbar_init(ds_full, 1);
     mbar_init(g_full, 1);
     mbar_init(p_full, 8);
     mbar_init(s_full, 4);
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
     mbar_init(done, 2);
     fence_barrier_init();
   }
-  if (warp == 25) tmem_alloc(holder, 512);
+  if (warp == 29) tmem_alloc(holder, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -196,8 +197,8 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   const uint32_t base = smem_u32(sm);
   const float* scal = reinterpret_cast<const float*>(sm + Y::kSc);
 
-  if (warp >= 24) {
-    if (warp == 24) {
+  if (warp >= 28) {
+    if (warp == 28) {
       // ---------------------------------------------------------------- product dS
       // A = keys read MN-major (key columns along M; for d_k <= 64 the upper 64 rows read the next
       // tile and are not used), B = the three parts of W V one after the other; two buffers
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
             }
             umma_commit(&xw_free[u]);
             if (u == 1) {
-              umma_commit(ds_full);
+              umma_commit(&ds_full[i & 1]);
               umma_commit(&kq_free[s]);
               umma_commit(&sc_free[s]);
               if (!FULL) umma_commit(&v_done[s]);
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 60, 0);
       if (elect_one()) umma_commit(done);
       __syncwarp();
-    } else if (warp == 25) {
+    } else if (warp == 29) {
       // ---------------------------------------------------------------- products Y1, G, Y2
       if (FULL) {
         const uint32_t id_g = idesc_bf16_f32(128, 128);
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       __syncwarp();
       mbar_wait_bounded(done, 0);              // both issuers, before tensor memory is released
       __syncwarp();
-    } else if (warp == 26) {
+    } else if (warp == 30) {
       // ---------------------------------------------------------------- values
       if (lane == 0) {
         prefetch_tmap(&c.mv);
@@ -468,9 +469,9 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       }
       if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 62, 0);
     }
-  } else if (warp >= 16 && warp < 20) {
+  } else if (warp >= 16 && warp < 24) {
     // ------------------------------------------------------------------ W V
-    const int w4 = warp & 3, t = 32 * w4 + lane;
+    const int w4 = warp & 3, t = 32 * w4 + lane, q0 = 4 * ((warp - 16) >> 2);
     bool ok = true;
     for (int i = 0; i < nch; ++i) {
       const int s = i % NST, n = i / NST;
@@ -491,20 +492,21 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         ok = warp_wait(&kq_full[s], n);
         if (!ok) break;
         if (!live) {
+          const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-          for (int q = 0; q < 8; ++q) {
-            reinterpret_cast<uint4*>(vrow)[q] = make_uint4(0, 0, 0, 0);
+          for (int q = q0; q < q0 + 4; ++q) {
+            const uint32_t off = uint32_t((q ^ (t & 7)) << 4);
+            *reinterpret_cast<uint4*>(vrow + off) = z;
 #pragma unroll
             for (int b = 0; b < KB; ++b)
-              reinterpret_cast<uint4*>(sm + s * Y::kKQ + b * kBlk + t * 128)[q] =
-                  make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(sm + s * Y::kKQ + b * kBlk + t * 128 + off) = z;
           }
         }
       }
       // a product of 24 bits is its upper 8 bits, the next 8 and the rest, each cut off exactly
-      uint4 nx = *reinterpret_cast<const uint4*>(vrow + ((t & 7) << 4));
-#pragma unroll 2
-      for (int q = 0; q < 8; ++q) {
+      uint4 nx = *reinterpret_cast<const uint4*>(vrow + ((q0 ^ (t & 7)) << 4));
+#pragma unroll 1
+      for (int q = q0; q < q0 + 4; ++q) {
         const uint32_t off = uint32_t((q ^ (t & 7)) << 4);
         const uint32_t vw[4] = {nx.x, nx.y, nx.z, nx.w};
         nx = *reinterpret_cast<const uint4*>(vrow + ((((q + 1) & 7) ^ (t & 7)) << 4));
@@ -537,9 +539,9 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       }
     }
     if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 63, 0);
-  } else if (warp >= 20) {
+  } else if (warp >= 24) {
     // ------------------------------------------------------------------ state rows
-    const int k = tid - 640, w4 = warp - 20;
+    const int k = tid - 768, w4 = warp - 24;
     const uint32_t tl = tmem + (uint32_t(32 * w4) << 16);
     const bool mine = k < a.d_k, holds = k < 64 * KB;    // a key column, a row of the copy
     const float* entering = nullptr;
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       const bool slow = ex > -0.5f;
       const float mul1 = slow ? expm1f(ex) : expf(ex), keep1 = slow ? 1.f : 0.f;
       const uint64_t mul = f2(mul1, mul1), keep = f2(keep1, keep1);
-      ok = warp_wait(ds_full, i) && (!FULL || warp_wait(y_full, i));
+      ok = warp_wait(&ds_full[i & 1], i >> 1) && (!FULL || warp_wait(y_full, i));
       if (!ok) break;
       tc_fence_after();
 #pragma unroll 1
@@ -725,7 +727,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 25) {
+  if (warp == 29) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
