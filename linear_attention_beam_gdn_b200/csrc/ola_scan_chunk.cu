@@ -20,13 +20,13 @@
 // One block per (sequence, head, 64 value columns, piece), one per SM:
 //   warps 0-7    G -> P (thread = token t, half of the columns; P into tensor memory as the A
 //                operand of Y1); warps 0-3 also the next chunk's scalars (dt, running sums)
-//   warps 8-15   outputs (thread = token t, half of the columns): Y1 + e^{c_t} Y2, D, gate; y
-//                stored from registers
+//   warps 8-15   outputs (thread = token t, half of the columns): Y1 + e^{c_t} Y2, D, gate; y staged
+//                over v (rows of 32 scattered 16-byte stores would take half of the data pipe)
 //   warps 16-23  W V (thread = token s, half of the columns)
 //   warps 24-27  state rows (thread = key column, S^T in tensor memory): S = e^{c_C} S + dS and its
 //                bf16 copy
 //   warp 28      tcgen05.mma: dS;   warp 29  tcgen05.mma: Y1, the next chunk's G, Y2
-//   warp 30      TMA loads of v
+//   warp 30      TMA loads of v, stores of y
 //   warp 31      TMA loads of keys and queries
 // Two issuing warps, so that neither chain (G -> P -> Y1 and W V -> dS -> S -> Y2) waits behind the
 // other's operands; nothing but Y2 waits for the state. A piece of a cut sequence runs twice: dS alone first (FULL = false), then, once
@@ -62,15 +62,16 @@ struct Lay {
   static constexpr uint32_t kS = kXw + 3 * kBlk;           // state copy [64 KB rows][64 columns]
   static constexpr uint32_t kSc = kS + KB * 8192;          // scalars per stage
   static constexpr uint32_t kBar = kSc + NST * kScFloats * 4;
-  static constexpr int kNBar = 6 * NST + 14;
-  static constexpr uint32_t kBytes = kBar + kNBar * 8 + 16;
+  static constexpr int kNBar = 7 * NST + 14;
+  // the tensor-memory address is handed over in the scalars' place, before they are written
+  static constexpr uint32_t kBytes = kBar + kNBar * 8;
 };
 static_assert(Lay<1>::kBar % 8 == 0 && Lay<2>::kBar % 8 == 0, "mbarriers");
 static_assert(Lay<1>::kBytes <= 232448 && Lay<2>::kBytes <= 232448, "shared memory per block");
 static_assert((kScFloats * 4) % 16 == 0, "float4 rows of scalars");
 
 struct ChunkScan {
-  CUtensorMap mv, mk, mq;               // [R][P][heads][d] bf16, boxes of 64 x 1 x 128 x 1
+  CUtensorMap mv, mk, mq, my;           // [R][P][heads][d] bf16, boxes of 64 x 1 x 128 x 1
   ScanArgs a;
   int ntile;                            // blocks of 64 value columns
 };
@@ -106,6 +107,24 @@ __device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t (&v)[8]) {
       : "memory");
 }
 
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int c0,
+                                             int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::
+          "l"(reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;
   asm volatile(
@@ -132,10 +151,11 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   uint64_t* kq_full = bar;               // [NST] keys and queries landed (TMA bytes)
   uint64_t* kq_free = bar + NST;         // [NST] ... read by the products (one commit per issuer)
   uint64_t* v_full = bar + 2 * NST;      // [NST] values landed (TMA bytes)
-  uint64_t* v_done = bar + 3 * NST;      // [NST] values read (commit, 8 W V and 8 output warps); dS done if !FULL
+  uint64_t* v_done = bar + 3 * NST;      // [NST] y written over the values (8 warps); dS done if !FULL
   uint64_t* sc_full = bar + 4 * NST;     // [NST] scalars written (4 warps)
   uint64_t* sc_free = bar + 5 * NST;     // [NST] scalars read (commits, state and output warps)
-  uint64_t* one = bar + 6 * NST;
+  uint64_t* x_done = bar + 6 * NST;      // [NST] values read by the W V warps (8 warps)
+  uint64_t* one = bar + 7 * NST;
   uint64_t* xw_full = one + 0;           // [2] W V of 64 tokens written (4 warps)
   uint64_t* xw_free = one + 2;           // [2] ... read by dS (commit)
   uint64_t* ds_full = one + 4;           // [2] dS buffer done; one barrier per buffer: a state warp
@@ -147,7 +167,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   uint64_t* y_full = one + 11;           // Y1 and Y2 done
   uint64_t* y_free = one + 12;           // Y1 and Y2 read (8 warps)
   uint64_t* done = one + 13;             // every MMA completed (both issuers)
-  uint32_t* holder = reinterpret_cast<uint32_t*>(bar + Y::kNBar);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(sm + Y::kSc);
   const ScanArgs& a = c.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -171,7 +191,8 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       mbar_init(&kq_full[s], 1);
       mbar_init(&kq_free[s], FULL ? 2 : 1);
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_done[s], FULL ? 17 : 1);
+      mbar_init(&v_done[s], FULL ? 8 : 1);
+      mbar_init(&x_done[s], 8);
       mbar_init(&sc_full[s], 4);
       mbar_init(&sc_free[s], FULL ? 14 : 5);
     }
@@ -194,6 +215,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *holder;
+  __syncthreads();                         // read by all before the first scalars take its place
   const uint32_t base = smem_u32(sm);
   const float* scal = reinterpret_cast<const float*>(sm + Y::kSc);
 
@@ -295,7 +317,6 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
                 umma_bf16(tmem + kTY2, dq + (k >> 2) * (kBlk >> 4) + (k & 3) * 2, dsd + k * 128,
                           id_y, k != 0);
               umma_commit(y_full);
-              umma_commit(&v_done[s]);
               umma_commit(&kq_free[s]);
               umma_commit(&sc_free[s]);
             }
@@ -309,7 +330,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       mbar_wait_bounded(done, 0);              // both issuers, before tensor memory is released
       __syncwarp();
     } else if (warp == 30) {
-      // ---------------------------------------------------------------- values
+      // ---------------------------------------------------------------- values in, y out
       if (lane == 0) {
         prefetch_tmap(&c.mv);
         auto load = [&](int i) {
@@ -325,10 +346,18 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
             report_error(a.err, OLA_ERR_TIMEOUT, 66, i);
             break;
           }
+          // rows past P are clipped; a sequence that ends inside the chunk but before P was
+          // stored row by row
+          if (FULL && (p0 + (i + 1) * kQ <= p1 || p1 == a.P)) {
+            tma_store_4d(&c.my, sm + Y::kV + s * kBlk, kNV * tile, h, p0 + i * kQ, r);
+            bulk_commit();
+            bulk_wait_read();
+          }
           if (issued < nch) load(issued++);
         }
         for (int i = issued > NST ? issued - NST : 0; i < issued; ++i)
           mbar_wait_bounded(&v_full[i % NST], (i / NST) & 1);
+        if (FULL) bulk_wait_all();
       }
       __syncwarp();
     } else {
@@ -509,7 +538,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       for (int q = q0; q < q0 + 4; ++q) {
         const uint32_t off = uint32_t((q ^ (t & 7)) << 4);
         const uint32_t vw[4] = {nx.x, nx.y, nx.z, nx.w};
-        nx = *reinterpret_cast<const uint4*>(vrow + ((((q + 1) & 7) ^ (t & 7)) << 4));
+        if (q + 1 < q0 + 4) nx = *reinterpret_cast<const uint4*>(vrow + (((q + 1) ^ (t & 7)) << 4));
         uint32_t h1[4], h2[4], h3[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -535,7 +564,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&xw_full[w4 >> 1]);
-        if (FULL) mbar_arrive(&v_done[s]);
+        if (FULL) mbar_arrive(&x_done[s]);
       }
     }
     if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 63, 0);
@@ -674,8 +703,8 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         const uint64_t ec2 = f2(ec, ec);
         warp_arrive(&sc_free[s]);
         unsigned char* vrow = sm + Y::kV + s * kBlk + t * 128;
-        if (!skip) warp_arrive(&v_done[s]);
-        ok = warp_wait(y_full, i);
+        const bool by_tma = p0 + (i + 1) * kQ <= p1 || p1 == a.P;
+        ok = warp_wait(y_full, i) && warp_wait(&x_done[s], i / NST);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
@@ -714,13 +743,16 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
               ow[e] = pack2(o[e]);
             }
             const uint4 o4 = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-            if (live && 8 * (2 * hq + u) < nv)
+            if (by_tma)
+              *reinterpret_cast<uint4*>(at[u]) = o4;
+            else if (live && 8 * (2 * hq + u) < nv)
               *(reinterpret_cast<uint4*>(yp + int64_t(p) * a.y_tok) + 2 * hq + u) = o4;
           }
         }
         tc_fence_before();
         warp_arrive(y_free);
-        if (skip) warp_arrive(&v_done[s]);
+        fence_proxy_async_smem();
+        warp_arrive(&v_done[s]);
       }
       if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 65, 0);
     }
@@ -757,7 +789,8 @@ EncodeFn map_encoder() {
 }
 
 // [R][P][heads][d] bf16 with the given strides as a 4-D map (column, head, token, sequence) of
-// 64 x 1 x 128 x 1 boxes, 128-byte swizzle. Columns past d and tokens past P read 0.
+// 64 x 1 x 128 x 1 boxes, 128-byte swizzle. Columns past d and tokens past P read 0 and are not
+// written.
 bool rows_map(CUtensorMap* map, const void* base, int d, int heads, int P, int R, int64_t tok,
               int64_t seq) {
   EncodeFn fn = map_encoder();
@@ -832,7 +865,8 @@ cudaError_t launch_scan_chunk(const ScanArgs& a, cudaStream_t st) {
   c.ntile = (a.d_v + kNV - 1) / kNV;
   if (!rows_map(&c.mv, a.v, a.d_v, a.H, a.P, a.R, a.v_tok, a.v_seq) ||
       !rows_map(&c.mk, a.k, a.d_k, a.G, a.P, a.R, a.k_tok, a.k_seq) ||
-      !rows_map(&c.mq, a.q, a.d_k, a.G, a.P, a.R, a.q_tok, a.q_seq))
+      !rows_map(&c.mq, a.q, a.d_k, a.G, a.P, a.R, a.q_tok, a.q_seq) ||
+      !rows_map(&c.my, a.y, a.d_v, a.H, a.P, a.R, a.y_tok, a.y_seq))
     return cudaErrorInvalidValue;
   return a.d_k <= 64 ? run<1>(c, st) : run<2>(c, st);
 }
