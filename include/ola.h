@@ -261,7 +261,8 @@ ola_status ola_decode_noalloc(const ola_geometry* geom, const float* S_ctx, cons
  *
  * Conventions, beside those above:
  * - Asynchronous on `stream`, no allocation, no host synchronisation: every call can be captured
- *   into a CUDA graph. Outputs must not overlap inputs unless a function says so.
+ *   into a CUDA graph (the first call on each device looks up the library's error word: make it
+ *   before a capture). Outputs must not overlap inputs unless a function says so.
  * - Strides are in elements, "tok" between consecutive tokens (or beams) and "seq" between
  *   sequences; 0 stands for the contiguous value. Channels (heads x width) are contiguous.
  *   A tok stride is at least the row's width; a sequence may not overlap the next one in outputs.
@@ -289,7 +290,7 @@ ola_status ola_layer_status(void* stream);
  *   y         : [R][P][C] in_dtype (strides);  y and x may be column slices of one wide buffer,
  *               but not the same columns
  *   state_out : [R][W-1][C] in_dtype or NULL: the last W-1 tokens of u up to the sequence's end
- * R >= 1, P >= 0 (P = 0: state_out = state_in), C >= 1, W 2..4.
+ * R >= 1, P 0..2^30 (P = 0: state_out = state_in), C >= 1, W 2..4.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 typedef struct {
   int32_t R, P, C, W;
@@ -346,7 +347,7 @@ ola_status ola_qk_norm(const ola_qk_desc* d, const void* q, const void* k, const
  *   S_in    : [R][H][d_v][d_k] fp32 or NULL;  S_out : the same, or NULL; may be S_in itself
  *   ws      : device scratch of ola_scan_workspace_bytes(d) bytes, 16-byte aligned (NULL if 0).
  *             Calls that may overlap on the GPU need scratch of their own.
- * d_k, d_v in {16, 32, 64, 128, 256}, G divides H, P >= 0. dt * A is taken to be <= 0 (a decay);
+ * d_k, d_v in {16, 32, 64, 128, 256}, G divides H, R * H <= 2^24, P 0..2^30. dt * A is taken to be <= 0 (a decay);
  * growth is computed as the formula says as long as it does not overflow. States and sums are
  * fp32. bf16 prompts with 16-byte aligned rows and d_k <= 128 run in chunks of 128 tokens on
  * tensor cores: keys, queries and v enter exactly; the token-to-token weights and the copy of

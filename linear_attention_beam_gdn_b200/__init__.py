@@ -687,6 +687,9 @@ def _scan_args(v, dt, A, k, q, D, dt_bias, z, out, softplus, ix, code):
                   _opt(D, "D", hs, f32, ix), _opt(dt_bias, "dt_bias", hs, f32, ix), zp), yp
 
 
+_SCAN_WS = {}        # scratch bytes by shape and device (a pure function of them)
+
+
 def scan(v, dt, A, k, q, *, D=None, dt_bias=None, z=None, S_in=None, lens=None, softplus=True,
          out=None, S_out=None, stream=None):
     """Selective state space scan of a prompt (ola_scan): v [R, P, H, d_v], k, q [R, P, G, d_k]
@@ -704,7 +707,12 @@ def scan(v, dt, A, k, q, *, D=None, dt_bias=None, z=None, S_in=None, lens=None, 
         shape = (R, H, d_v, desc.d_k)
         if S_out is None:
             S_out = torch.empty(shape, device=v.device, dtype=torch.float32)
-        n = ola_scan_workspace_bytes(desc)
+        key = (R, P, H, desc.d_k, d_v, code, ix)
+        n = _SCAN_WS.get(key)
+        if n is None:
+            if len(_SCAN_WS) >= 4096:
+                _SCAN_WS.clear()
+            n = _SCAN_WS[key] = ola_scan_workspace_bytes(desc)
         ws = torch.empty((n,), device=v.device, dtype=torch.uint8) if n else None
         _check(ola_scan(desc, *ptrs, _opt(S_in, "S_in", shape, torch.float32, ix),
                         _opt(lens, "lens", (R,), torch.int32, ix), yp,

@@ -20,6 +20,7 @@ namespace {
 constexpr int kConvThreads = 256;
 constexpr int kConvUnroll = 4;      // tokens loaded together
 constexpr int kAhead = 3;           // groups of them in flight
+constexpr int kStepAhead = 3;       // beams in flight
 
 // fp32 pairs of a pack: VEC elements as (VEC + 1) / 2 pairs.
 template <typename T, int VEC>
@@ -231,49 +232,87 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvArgs a) {
 }
 
 // One token of every beam: thread = 16 bytes of channels x tt consecutive beams (of all requests).
+// 16-byte vectors come through a thread-private ring of kStepAhead beams (window and token), the
+// parent indices one beam further ahead.
 template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvArgs a) {
   extern __shared__ __align__(16) float sm[];
+  constexpr bool ASYNC = VEC * sizeof(T) == 16;
+  constexpr int kVecBytes = VEC * int(sizeof(T)), kSlot = kConvThreads * kVecBytes;
   const int ct = blockIdx.x % a.n_ctile;
   const int64_t tile = int64_t(blockIdx.x / a.n_ctile) * blockDim.y + threadIdx.y;
   const int nc = blockDim.x * VEC, c0 = ct * nc, cl = threadIdx.x * VEC, c = c0 + cl;
   const int64_t n = int64_t(a.R) * a.P;
-  const int64_t i0 = tile * a.tt, i1 = min(i0 + a.tt, n);
+  const int64_t i0 = c < a.C ? tile * a.tt : n, i1 = min(i0 + a.tt, n);
+  unsigned char* ring = reinterpret_cast<unsigned char*>(sm + (W + 1) * nc) +
+                        (threadIdx.y * blockDim.x + threadIdx.x) * kVecBytes;
+  // next beam to fetch: its request, beam and parent
+  int64_t in = i0;
+  int rn = int(i0 / a.P), bn = int(i0 - int64_t(rn) * a.P), slot_n = 0;
+  int pn = i0 < i1 ? parent_state(a.parent, rn, bn, a.P, a.Bp, a.err) : 0;
+  auto sources = [&](const T** si, const T** xp) {
+    *si = static_cast<const T*>(a.state_in) + (int64_t(rn) * a.Bp + pn) * (W - 1) * a.C + c;
+    *xp = static_cast<const T*>(a.x) + int64_t(rn) * a.x_seq + int64_t(bn) * a.x_tok + c;
+  };
+  auto advance = [&]() {
+    ++in;
+    if (++bn == a.P) {
+      bn = 0;
+      ++rn;
+    }
+    if (in < i1) pn = parent_state(a.parent, rn, bn, a.P, a.Bp, a.err);
+  };
+  auto fetch_async = [&]() {
+    if constexpr (ASYNC) {
+      if (in < i1) {
+        const T *si, *xp;
+        sources(&si, &xp);
+        unsigned char* dst = ring + slot_n * (W * kSlot);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) cp_async16(dst + j * kSlot, si + int64_t(j) * a.C);
+        cp_async16(dst + (W - 1) * kSlot, xp);
+        advance();
+      }
+      slot_n = slot_n + 1 < kStepAhead ? slot_n + 1 : 0;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kStepAhead; ++s) fetch_async();
   Taps<T, VEC, W> taps;
   taps.load(a, sm, c0, nc, cl);
-  if (c >= a.C || i0 >= i1) return;
-  for (int64_t i = i0; i < i1; i += 2) {           // two beams' loads together
-    Pack<T, VEC> s[2][W - 1], x[2];
-    int64_t yo[2];
+  int r = int(i0 / a.P), b = int(i0 - int64_t(r) * a.P), slot = 0;
+  T* so = static_cast<T*>(a.state_out) + i0 * (W - 1) * a.C + c;
+#pragma unroll 1
+  for (int64_t i = i0; i < i1; ++i) {
+    Pack<T, VEC> s[W];
+    if constexpr (ASYNC) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStepAhead - 1) : "memory");
+      const unsigned char* src = ring + slot * (W * kSlot);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      x[u].zero();
-      yo[u] = -1;
-      if (i + u >= i1) continue;
-      const int r = int((i + u) / a.P), b = int(i + u - int64_t(r) * a.P);
-      const int p = parent_state(a.parent, r, b, a.P, a.Bp, a.err);
-      const T* si = static_cast<const T*>(a.state_in) +
-                    (int64_t(r) * a.Bp + p) * (W - 1) * a.C + c;
+      for (int j = 0; j < W; ++j) s[j].load(reinterpret_cast<const T*>(src + j * kSlot));
+      slot = slot + 1 < kStepAhead ? slot + 1 : 0;
+      fetch_async();
+    } else {
+      const T *si, *xp;
+      sources(&si, &xp);
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j) s[u][j].load(si + int64_t(j) * a.C);
-      x[u].load(static_cast<const T*>(a.x) + int64_t(r) * a.x_seq + int64_t(b) * a.x_tok + c);
-      yo[u] = int64_t(r) * a.y_seq + int64_t(b) * a.y_tok + c;
+      for (int j = 0; j < W - 1; ++j) s[j].load(si + int64_t(j) * a.C);
+      s[W - 1].load(xp);
+      advance();
     }
+    Pairs<T, VEC> u[W], yf;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (yo[u] < 0) break;
-      Pairs<T, VEC> win[W - 1], xf, yf;
+    for (int j = 0; j < W; ++j) u[j].from(s[j]);
+    taps.apply(u, u[W - 1], a.silu, yf);
+    Pack<T, VEC> o;
+    yf.to(o);
+    o.store(static_cast<T*>(a.y) + int64_t(r) * a.y_seq + int64_t(b) * a.y_tok + c);
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j) win[j].from(s[u][j]);
-      xf.from(x[u]);
-      taps.apply(win, xf, a.silu, yf);
-      Pack<T, VEC> o;
-      yf.to(o);
-      o.store(static_cast<T*>(a.y) + yo[u]);
-      T* so = static_cast<T*>(a.state_out) + (i + u) * (W - 1) * a.C + c;
-#pragma unroll
-      for (int j = 0; j < W - 2; ++j) s[u][j + 1].store(so + int64_t(j) * a.C);
-      x[u].store(so + int64_t(W - 2) * a.C);
+    for (int j = 0; j < W - 1; ++j, so += a.C) s[j + 1].store(so);
+    if (++b == a.P) {
+      b = 0;
+      ++r;
     }
   }
 }
@@ -281,21 +320,18 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvArgs a) {
 template <typename T, int VEC, int W>
 cudaError_t run(const ConvArgs& a, bool step, dim3 block, unsigned grid, cudaStream_t st) {
   const size_t smem = sizeof(float) * (W + 1) * block.x * VEC;
-  if (step) {
-    conv_step_kernel<T, VEC, W><<<grid, block, smem, st>>>(a);
-  } else {
-    constexpr size_t ring =
-        VEC * sizeof(T) == 16 ? size_t(kAhead) * kConvUnroll * kConvThreads * 16 : 0;
-    if (smem + ring > 48 * 1024) {
-      static std::atomic<uint64_t> done{0};
-      cudaError_t e = once_per_device(done, [] {
-        return cudaFuncSetAttribute(conv_kernel<T, VEC, W>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
-      });
-      if (e != cudaSuccess) return e;
-    }
-    conv_kernel<T, VEC, W><<<grid, block, smem + ring, st>>>(a);
+  constexpr bool ASYNC = VEC * sizeof(T) == 16;
+  constexpr size_t slot = size_t(kConvThreads) * 16;
+  const size_t ring = ASYNC ? slot * (step ? kStepAhead * W : kAhead * kConvUnroll) : 0;
+  auto kernel = step ? conv_step_kernel<T, VEC, W> : conv_kernel<T, VEC, W>;
+  if (smem + ring > 48 * 1024) {
+    static std::atomic<uint64_t> done[2] = {};
+    cudaError_t e = once_per_device(done[step], [&] {
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 80 * 1024);
+    });
+    if (e != cudaSuccess) return e;
   }
+  kernel<<<grid, block, smem + ring, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -322,7 +358,7 @@ cudaError_t launch(ConvArgs a, int in_dtype, int W, bool wide, bool step, cudaSt
   // tokens (beams) per thread: as many as leave about 8 blocks for every SM
   const int64_t rows = step ? int64_t(a.R) * a.P : a.P;
   const int64_t seqs = step ? 1 : a.R;
-  a.tt = step ? 16 : 32;
+  a.tt = step ? 8 : 32;
   const int least = step ? 2 : 4;
   const int64_t least_blocks = int64_t(step || !wide ? 8 : 1) * sms;
   auto blocks = [&](int tt) {

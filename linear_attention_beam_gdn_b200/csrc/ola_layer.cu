@@ -98,7 +98,8 @@ ola_status conv_args(const ola_conv_desc* d, const void* x, const float* w, cons
   if (!d || !w) return OLA_ERR_INVALID_ARG;
   if (d->R < 1 || d->P < 0 || d->C < 1 || !dtype_ok(d->in_dtype) || (d->silu & ~1))
     return OLA_ERR_INVALID_ARG;
-  if (d->W < 2 || d->W > 4) return OLA_ERR_UNSUPPORTED;
+  // token indices, and those of a tile past the end, are 32-bit
+  if (d->W < 2 || d->W > 4 || d->P > (1 << 30)) return OLA_ERR_UNSUPPORTED;
   if (d->P > 0 && (!x || !y)) return OLA_ERR_INVALID_ARG;
   const int e = d->in_dtype == OLA_BF16 ? 2 : 4;
   *rx = Rows{x, d->R, d->P, d->x_tok, d->x_seq, d->C, e};
@@ -133,7 +134,7 @@ ola_status scan_shape(const ola_scan_desc* d) {
     return OLA_ERR_INVALID_ARG;
   if (!width_ok(d->d_k) || !width_ok(d->d_v)) return OLA_ERR_UNSUPPORTED;
   // blocks and (sequence, head, piece) indices are 32-bit
-  if (int64_t(d->R) * d->H > (int64_t(1) << 24)) return OLA_ERR_UNSUPPORTED;
+  if (int64_t(d->R) * d->H > (int64_t(1) << 24) || d->P > (1 << 30)) return OLA_ERR_UNSUPPORTED;
   return OLA_OK;
 }
 

@@ -60,6 +60,31 @@ struct ScanArgs {
   int* err;
 };
 
+// Programmatic dependent launch: a kernel launched with launch_dependent may start while the one
+// before it on the stream still runs, and waits for its results only where it reads them.
+__device__ __forceinline__ void wait_for_previous_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_kernel_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <typename... Args, typename... Given>
+cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem,
+                             cudaStream_t st, const Given&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, Args(args)...);
+}
+
 // Tokens of sequence r.
 __device__ __forceinline__ int seq_len(const int* lens, int r, int P) {
   return lens ? min(max(__ldg(lens + r), 0), P) : P;

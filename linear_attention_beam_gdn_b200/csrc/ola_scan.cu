@@ -54,21 +54,26 @@ __device__ __forceinline__ void load_seg(const T* row, int lt, uint64_t (&x)[SEG
 }
 
 // Copies `n` rows of `width` elements (source rows `stride` apart) to consecutive rows in shared
-// memory: 16-byte asynchronous copies if `wide`, else element by element.
+// memory: 16-byte asynchronous copies if `wide`, else element by element. Rows n .. kTC - 1 are set
+// to zero, so that the arithmetic needs no bound.
 template <typename T>
 __device__ __forceinline__ void stage(T* dst, const T* src, int64_t stride, int n, int width,
                                       bool wide) {
+  constexpr int E = 16 / int(sizeof(T));
   if (wide) {
-    constexpr int E = 16 / int(sizeof(T));
-    const int per = width / E;
-    for (int i = threadIdx.x; i < n * per; i += kScanThreads) {
-      const int t = i / per, c = (i - t * per) * E;
-      cp_async16(dst + t * width + c, src + int64_t(t) * stride + c);
+    const int shift = __ffs(width / E) - 1;        // widths are powers of two
+    for (int i = threadIdx.x; i < kTC << shift; i += kScanThreads) {
+      const int t = i >> shift, c = (i - (t << shift)) * E;
+      if (t < n)
+        cp_async16(dst + t * width + c, src + int64_t(t) * stride + c);
+      else
+        *reinterpret_cast<uint4*>(dst + t * width + c) = make_uint4(0, 0, 0, 0);
     }
   } else {
-    for (int i = threadIdx.x; i < n * width; i += kScanThreads) {
-      const int t = i / width, c = i - t * width;
-      dst[i] = src[int64_t(t) * stride + c];
+    const int shift = __ffs(width) - 1;
+    for (int i = threadIdx.x; i < kTC << shift; i += kScanThreads) {
+      const int t = i >> shift, c = i - (t << shift);
+      dst[i] = t < n ? src[int64_t(t) * stride + c] : from_f32<T>(0.f);
     }
   }
 }
@@ -103,7 +108,35 @@ __global__ void __launch_bounds__(kScanThreads) scan_tok_kernel(ScanArgs a, int 
   const float* dtp = a.dt + int64_t(r) * a.P * a.H + h;
   const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, D = a.D ? a.D[h] : 0.f;
 
+  auto k_of = [&](int b) { return stages + b * kStageElems; };
+  auto v_of = [&](int b) { return stages + b * kStageElems + kTC * DK * (FULL ? 2 : 1); };
+  auto load_dt = [&](int pt) -> float {            // one tile ahead of its use
+    return tid < kTC && pt + tid < p1 ? dtp[int64_t(pt + tid) * a.H] : 0.f;
+  };
+  float raw = load_dt(p0);
+  auto copy_tile = [&](int pt, int b) {
+    const int np = min(kTC, p1 - pt);
+    stage<T>(k_of(b), kp + int64_t(pt) * a.k_tok, a.k_tok, np, DK, wide);
+    stage<T>(v_of(b), vp + int64_t(pt) * a.v_tok, a.v_tok, np, nrow, wide);
+    if (FULL) {
+      stage<T>(k_of(b) + kTC * DK, qp + int64_t(pt) * a.q_tok, a.q_tok, np, DK, wide);
+      if (zp) stage<T>(v_of(b) + kTC * ROWS, zp + int64_t(pt) * a.z_tok, a.z_tok, np, nrow, wide);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (tid < kTC) {
+      float dt = raw + bias;
+      if (a.softplus) dt = softplus_f(dt);
+      if (tid >= np) dt = 0.f;
+      raw = load_dt(pt + kTC);
+      ds[b * kTC + tid] = dt;
+      as[b * kTC + tid] = expf(dt * A);
+    }
+  };
+  double logsum = 0.0;                             // sum of dt A over the piece
+  if (p0 < p1) copy_tile(p0, 0);
   const float* entering = nullptr;
+  if (FULL && a.nseg > 1) wait_for_previous_kernel();
+  if (!FULL) let_next_kernel_start();
   if (FULL)
     entering = a.nseg > 1 ? a.seg_S + (int64_t(rh) * a.nseg + seg) * a.d_v * DK
                           : (a.S_in ? a.S_in + int64_t(rh) * a.d_v * DK : nullptr);
@@ -117,29 +150,6 @@ __global__ void __launch_bounds__(kScanThreads) scan_tok_kernel(ScanArgs a, int 
       S[j][i] = entering && row < nrow ? f2(e[0], e[1]) : f2(0.f, 0.f);
     }
   }
-  auto k_of = [&](int b) { return stages + b * kStageElems; };
-  auto v_of = [&](int b) { return stages + b * kStageElems + kTC * DK * (FULL ? 2 : 1); };
-  auto copy_tile = [&](int pt, int b) {
-    const int np = min(kTC, p1 - pt);
-    stage<T>(k_of(b), kp + int64_t(pt) * a.k_tok, a.k_tok, np, DK, wide);
-    stage<T>(v_of(b), vp + int64_t(pt) * a.v_tok, a.v_tok, np, nrow, wide);
-    if (FULL) {
-      stage<T>(k_of(b) + kTC * DK, qp + int64_t(pt) * a.q_tok, a.q_tok, np, DK, wide);
-      if (zp) stage<T>(v_of(b) + kTC * ROWS, zp + int64_t(pt) * a.z_tok, a.z_tok, np, nrow, wide);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    if (tid < kTC) {
-      float dt = 0.f;
-      if (tid < np) {
-        dt = dtp[int64_t(pt + tid) * a.H] + bias;
-        if (a.softplus) dt = softplus_f(dt);
-      }
-      ds[b * kTC + tid] = dt;
-      as[b * kTC + tid] = expf(dt * A);
-    }
-  };
-  double logsum = 0.0;                             // sum of dt A over the piece
-  if (p0 < p1) copy_tile(p0, 0);
   int b = 0;
   for (int pt = p0; pt < p1; pt += kTC, b ^= 1) {
     const int np = min(kTC, p1 - pt);
@@ -161,7 +171,6 @@ __global__ void __launch_bounds__(kScanThreads) scan_tok_kernel(ScanArgs a, int 
         const int t = t0 + u;
 #pragma unroll
         for (int j = 0; j < RV; ++j) o[j][u] = 0.f;
-        if (t >= np) continue;
         uint64_t kk[SEG / 2], qq[FULL ? SEG / 2 : 1];
         load_seg<T, SEG>(ks + t * DK, lt, kk);
         if constexpr (FULL) load_seg<T, SEG>(qs + t * DK, lt, qq);
@@ -256,6 +265,8 @@ __global__ void __launch_bounds__(kScanThreads) scan_tok_kernel(ScanArgs a, int 
 __global__ void __launch_bounds__(256) scan_join_kernel(ScanArgs a) {
   const int64_t n4 = int64_t(a.d_v) * a.d_k / 4;
   const int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  let_next_kernel_start();
+  wait_for_previous_kernel();
   if (at >= n4 * a.R * a.H) return;
   const int64_t rh = at / n4, e4 = at - rh * n4;
   float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -264,18 +275,28 @@ __global__ void __launch_bounds__(256) scan_join_kernel(ScanArgs a) {
     e = make_float4(p[0], p[1], p[2], p[3]);
   }
   float4* s = reinterpret_cast<float4*>(a.seg_S) + rh * a.nseg * n4 + e4;
-  for (int i = 0; i < a.nseg; ++i, s += n4) {
-    if (i + 1 == a.nseg) {
-      *s = e;
-      break;
+  const float* al = a.seg_a + rh * a.nseg;
+  constexpr int kAhead = 8;                        // pieces loaded together
+  for (int i0 = 0; i0 < a.nseg; i0 += kAhead) {
+    float4 own[kAhead];
+    float d[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i0 + i + 1 < a.nseg) {
+        own[i] = s[i * n4];
+        d[i] = al[i0 + i];
+      }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i >= a.nseg) break;
+      s[i * n4] = e;
+      if (i0 + i + 1 == a.nseg) break;
+      e.x = fmaf(d[i], e.x, own[i].x);
+      e.y = fmaf(d[i], e.y, own[i].y);
+      e.z = fmaf(d[i], e.z, own[i].z);
+      e.w = fmaf(d[i], e.w, own[i].w);
     }
-    const float4 own = *s;
-    const float al = a.seg_a[rh * a.nseg + i];
-    *s = e;
-    e.x = fmaf(al, e.x, own.x);
-    e.y = fmaf(al, e.y, own.y);
-    e.z = fmaf(al, e.z, own.z);
-    e.w = fmaf(al, e.w, own.w);
+    s += kAhead * n4;
   }
 }
 
@@ -303,11 +324,17 @@ cudaError_t run(const ScanArgs& a, int wide, cudaStream_t st) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((e = launch_scan_join(a, st)) != cudaSuccess) return e;
   }
+  // the outputs of a piece can start before its entering state is there
+  if (a.nseg > 1)
+    return launch_dependent(scan_tok_kernel<T, SEG, RV, true>, grid, kScanThreads, full, st, a,
+                            wide);
   scan_tok_kernel<T, SEG, RV, true><<<grid, kScanThreads, full, st>>>(a, wide);
   return cudaGetLastError();
 }
 
-// Rows per block: 64, or what d_v needs; 32 where d_k = 256 would take too many registers.
+// Rows per block: 64, or what d_v needs; 32 where d_k = 256 would take too many registers. (32 rows
+// where blocks of 64 leave fewer than four per SM measured 5 % slower: the loads of keys and queries
+// are shared by half the rows.)
 template <typename T, int SEG>
 cudaError_t by_rows(const ScanArgs& a, int wide, cudaStream_t st) {
   if (a.d_v <= 16) return run<T, SEG, 1>(a, wide, st);
@@ -331,17 +358,17 @@ cudaError_t by_width(const ScanArgs& a, int wide, cudaStream_t st) {
 
 cudaError_t launch_scan_join(const ScanArgs& a, cudaStream_t st) {
   const int64_t n = int64_t(a.R) * a.H * a.d_v * a.d_k / 4;
-  scan_join_kernel<<<unsigned((n + 255) / 256), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(scan_join_kernel, unsigned((n + 255) / 256), 256, 0, st, a);
 }
 
 // Pieces: while the sequences alone leave most of the machine idle (fewer than 4 blocks per SM),
-// as many as fill it, of at least 64 tokens each.
+// as many as fill it, of at least 16 tokens each (777 tokens of 18 chains of 64 x 32: 21.6 us, with
+// at least 32 tokens 24.4 us, 64 tokens 29.0 us).
 void scan_tok_pieces(int R, int P, int H, int d_k, int d_v, int sms, int* nseg, int* seg_len) {
   const int64_t chains = int64_t(R) * H * ((d_v + 63) / 64);
   int64_t want = int64_t(4) * sms / chains;
-  if (want > P / 64) want = P / 64;
-  if (want < 2) want = 1;
+  if (want > P / 16) want = P / 16;
+  if (want < 4) want = 1;             // the first run costs two thirds of the second
   int64_t len = (int64_t(P) + want - 1) / want;
   len = (len + kTC - 1) / kTC * kTC;
   if (len < kTC) len = kTC;

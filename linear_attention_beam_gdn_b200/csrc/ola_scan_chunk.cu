@@ -20,11 +20,12 @@
 // One block per (sequence, head, 64 value columns, piece), one per SM:
 //   warps 0-7    G -> P (thread = token t, half of the columns; P into tensor memory as the A
 //                operand of Y1); warps 0-3 also the next chunk's scalars (dt, running sums)
-//   warps 8-15   outputs (thread = token t, half of the columns): Y1 + e^{c_t} Y2, D, gate; y staged
-//                over v (rows of 32 scattered 16-byte stores would take half of the data pipe)
+//   outputs (thread = token t): Y1 + e^{c_t} Y2, D, gate; y staged over v (rows of 32 scattered
+//                16-byte stores would take half of the data pipe)
+//   state rows (thread = key column, S^T in tensor memory): S = e^{c_C} S + dS and its bf16 copy
+//                these two share warps 8-15, half of the columns each, and 24-27: a gate makes the
+//                outputs the longer work, without one the state's chain is
 //   warps 16-23  W V (thread = token s, half of the columns)
-//   warps 24-27  state rows (thread = key column, S^T in tensor memory): S = e^{c_C} S + dS and its
-//                bf16 copy
 //   warp 28      tcgen05.mma: dS;   warp 29  tcgen05.mma: Y1, the next chunk's G, Y2
 //   warp 30      TMA loads of v, stores of y
 //   warp 31      TMA loads of keys and queries
@@ -43,9 +44,8 @@ constexpr int kThr = 1024;
 constexpr uint32_t kBlk = kQ * 128;     // 16 KB: 128 rows of 64 bf16 columns
 
 // tensor memory columns
-constexpr uint32_t kTG = 0;             // G, 128
-constexpr uint32_t kTP = 128;           // P as bf16 pairs, 64
-constexpr uint32_t kTD = 192;           // dS, two buffers of 64
+constexpr uint32_t kTG = 0;             // G, 128; P of 16 tokens (8 columns of bf16 pairs) in their place
+constexpr uint32_t kTD = 128;           // dS of the three parts of W V, 64 each
 constexpr uint32_t kTS = 320;           // S^T fp32, 64
 constexpr uint32_t kTY1 = 384;
 constexpr uint32_t kTY2 = 448;
@@ -62,7 +62,7 @@ struct Lay {
   static constexpr uint32_t kS = kXw + 3 * kBlk;           // state copy [64 KB rows][64 columns]
   static constexpr uint32_t kSc = kS + KB * 8192;          // scalars per stage
   static constexpr uint32_t kBar = kSc + NST * kScFloats * 4;
-  static constexpr int kNBar = 7 * NST + 14;
+  static constexpr int kNBar = 7 * NST + 12;
   // the tensor-memory address is handed over in the scalars' place, before they are written
   static constexpr uint32_t kBytes = kBar + kNBar * 8;
 };
@@ -96,6 +96,21 @@ __device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, uint32_t (
       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]),
         "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3]), "=r"(y[4]), "=r"(y[5]), "=r"(y[6]), "=r"(y[7]), "=r"(y[8]), "=r"(y[9]), "=r"(y[10]), "=r"(y[11]), "=r"(y[12]), "=r"(y[13]), "=r"(y[14]), "=r"(y[15])
       : "r"(ta), "r"(tb)
+      : "memory");
+}
+
+// 8 columns each of the three parts of dS (64 columns apart) and of S, one wait.
+__device__ __forceinline__ void tmem_ld8x4(uint32_t td, uint32_t (&a)[8], uint32_t (&b)[8],
+                                           uint32_t (&c)[8], uint32_t ts, uint32_t (&s)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%33];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%34];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24, %25, %26, %27, %28, %29, %30, %31}, [%35];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]),
+        "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]), "=r"(c[4]), "=r"(c[5]), "=r"(c[6]), "=r"(c[7]), "=r"(s[0]), "=r"(s[1]), "=r"(s[2]), "=r"(s[3]), "=r"(s[4]), "=r"(s[5]), "=r"(s[6]), "=r"(s[7])
+      : "r"(td), "r"(td + 64), "r"(td + 128), "r"(ts)
       : "memory");
 }
 
@@ -151,25 +166,25 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   uint64_t* kq_full = bar;               // [NST] keys and queries landed (TMA bytes)
   uint64_t* kq_free = bar + NST;         // [NST] ... read by the products (one commit per issuer)
   uint64_t* v_full = bar + 2 * NST;      // [NST] values landed (TMA bytes)
-  uint64_t* v_done = bar + 3 * NST;      // [NST] y written over the values (8 warps); dS done if !FULL
+  uint64_t* v_done = bar + 3 * NST;      // [NST] y written over the values (NY warps); dS done if !FULL
   uint64_t* sc_full = bar + 4 * NST;     // [NST] scalars written (4 warps)
   uint64_t* sc_free = bar + 5 * NST;     // [NST] scalars read (commits, state and output warps)
   uint64_t* x_done = bar + 6 * NST;      // [NST] values read by the W V warps (8 warps)
   uint64_t* one = bar + 7 * NST;
   uint64_t* xw_full = one + 0;           // [2] W V of 64 tokens written (4 warps)
   uint64_t* xw_free = one + 2;           // [2] ... read by dS (commit)
-  uint64_t* ds_full = one + 4;           // [2] dS buffer done; one barrier per buffer: a state warp
-                                         // may be a chunk behind the product
-  uint64_t* ds_free = one + 6;           // [2] dS buffer read (4 warps)
-  uint64_t* g_full = one + 8;            // G done, and Y1 of the chunk before
-  uint64_t* p_full = one + 9;            // G read and P written (8 warps)
-  uint64_t* s_full = one + 10;           // state copy written (4 warps)
-  uint64_t* y_full = one + 11;           // Y1 and Y2 done
-  uint64_t* y_free = one + 12;           // Y1 and Y2 read (8 warps)
-  uint64_t* done = one + 13;             // every MMA completed (both issuers)
+  uint64_t* ds_full = one + 4;           // dS done
+  uint64_t* ds_free = one + 5;           // dS read (NS warps)
+  uint64_t* g_full = one + 6;            // G done, and Y1 of the chunk before
+  uint64_t* p_full = one + 7;            // G read and P written (8 warps)
+  uint64_t* s_full = one + 8;            // state copy written (NS warps)
+  uint64_t* y_full = one + 9;            // Y1 and Y2 done
+  uint64_t* y_free = one + 10;           // Y1 and Y2 read (NY warps)
+  uint64_t* done = one + 11;             // every MMA completed (both issuers)
   uint32_t* holder = reinterpret_cast<uint32_t*>(sm + Y::kSc);
   const ScanArgs& a = c.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int NY = GATE ? 8 : 4, NS = 12 - NY;       // output and state warps
 
   // block -> (sequence, head, value columns, piece); neighbours share keys and queries
   const int nseg = FULL ? a.nseg : a.nseg - 1;
@@ -191,22 +206,22 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       mbar_init(&kq_full[s], 1);
       mbar_init(&kq_free[s], FULL ? 2 : 1);
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_done[s], FULL ? 8 : 1);
+      mbar_init(&v_done[s], FULL ? NY : 1);
       mbar_init(&x_done[s], 8);
       mbar_init(&sc_full[s], 4);
-      mbar_init(&sc_free[s], FULL ? 14 : 5);
+      mbar_init(&sc_free[s], FULL ? 2 + NY + NS : 1 + NS);
     }
     for (int u = 0; u < 2; ++u) {
       mbar_init(&xw_full[u], 4);
       mbar_init(&xw_free[u], 1);
-      mbar_init(&ds_full[u], 1);
-      mbar_init(&ds_free[u], 4);
     }
+    mbar_init(ds_full, 1);
+    mbar_init(ds_free, NS);
     mbar_init(g_full, 1);
     mbar_init(p_full, 8);
-    mbar_init(s_full, 4);
+    mbar_init(s_full, NS);
     mbar_init(y_full, 1);
-    mbar_init(y_free, 8);
+    mbar_init(y_free, NY);
     mbar_init(done, 2);
     fence_barrier_init();
   }
@@ -214,6 +229,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (!FULL) let_next_kernel_start();
   const uint32_t tmem = *holder;
   __syncthreads();                         // read by all before the first scalars take its place
   const uint32_t base = smem_u32(sm);
@@ -223,14 +239,12 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
     if (warp == 28) {
       // ---------------------------------------------------------------- product dS
       // A = keys read MN-major (key columns along M; for d_k <= 64 the upper 64 rows read the next
-      // tile and are not used), B = the three parts of W V one after the other; two buffers
-      const uint32_t id_d = idesc_bf16_f32_amn(128, kNV) | (1u << 16);           // A, B MN-major
+      // tile and are not used), B = the three parts of W V side by side: the keys are read once
+      const uint32_t id_d = idesc_bf16_f32_amn(128, 3 * kNV) | (1u << 16);       // A, B MN-major
       bool ok = true;
       for (int i = 0; i < nch; ++i) {
         const int s = i % NST;
-        const uint32_t dst = tmem + kTD + kNV * (i & 1);
-        ok = warp_wait(&kq_full[s], i / NST) &&
-             (i < 2 || warp_wait(&ds_free[i & 1], (i >> 1) - 1));
+        ok = warp_wait(&kq_full[s], i / NST) && (i == 0 || warp_wait(ds_free, i - 1));
 #pragma unroll 1
         for (int u = 0; u < 2 && ok; ++u) {              // 64 tokens each
           ok = warp_wait(&xw_full[u], i);
@@ -240,15 +254,11 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
             const uint64_t dk = sw128_mnmajor_desc(base + s * Y::kKQ + u * 8192, kBlk, 1024);
             const uint64_t dx = sw128_mnmajor_desc(base + Y::kXw + u * 8192, kBlk, 1024);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-#pragma unroll
-              for (int part = 0; part < 3; ++part)
-                umma_bf16(dst, dk + k * 128, dx + part * (kBlk >> 4) + k * 128, id_d,
-                          u != 0 || k != 0 || part != 0);
-            }
+            for (int k = 0; k < 4; ++k)
+              umma_bf16(tmem + kTD, dk + k * 128, dx + k * 128, id_d, u != 0 || k != 0);
             umma_commit(&xw_free[u]);
             if (u == 1) {
-              umma_commit(&ds_full[i & 1]);
+              umma_commit(ds_full);
               umma_commit(&kq_free[s]);
               umma_commit(&sc_free[s]);
               if (!FULL) umma_commit(&v_done[s]);
@@ -282,7 +292,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
               const uint64_t dv = sw128_mnmajor_desc(base + Y::kV + s * kBlk, kBlk, 1024);
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                umma_bf16_ts(tmem + kTY1, tmem + kTP + k * 8, dv + k * 128, id_y, k != 0);
+                umma_bf16_ts(tmem + kTY1, tmem + kTG + k * 16, dv + k * 128, id_y, k != 0);
             }
             __syncwarp();
           }
@@ -432,13 +442,6 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       for (int i = 1; i < nch && ok && c0 == 0; ++i) ok = scalars(i);
       if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 67, 0);
     } else {
-      {
-        const uint32_t z[8] = {};
-#pragma unroll 1
-        for (int j = w4 + 1; j < 4; ++j)                 // above the diagonal
-          tmem_st8(tl + kTP + 16 * j + (c0 >> 1), z);
-        tmem_st_wait();
-      }
       // s <= t within t's own block, as bits of the packed pairs
       uint32_t keep[8];
 #pragma unroll
@@ -471,7 +474,12 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
             p[2 * q] = pack2(mul2(f2(x[4 * q], x[4 * q + 1]), w0)) & keep[2 * q];
             p[2 * q + 1] = pack2(mul2(f2(x[4 * q + 2], x[4 * q + 3]), w1)) & keep[2 * q + 1];
           }
-          tmem_st8(tl + kTP + (col >> 1), p);
+          tmem_st8(tl + kTG + col, p);
+        }
+        {
+          const uint32_t z[8] = {};
+#pragma unroll 1
+          for (int j = w4 + 1; j < 4; ++j) tmem_st8(tl + kTG + 32 * j + c0, z);   // s > t
         }
         float mid = bs[w4] - mine;           // log2 decay from the end of block j to t
 #pragma unroll 1
@@ -489,7 +497,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
             p[2 * q] = pack2(mul2(f2(x[4 * q], x[4 * q + 1]), mul2(rf, c2.x)));
             p[2 * q + 1] = pack2(mul2(f2(x[4 * q + 2], x[4 * q + 3]), mul2(rf, c2.y)));
           }
-          tmem_st8(tl + kTP + (col >> 1), p);
+          tmem_st8(tl + kTG + col, p);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -568,12 +576,16 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       }
     }
     if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 63, 0);
-  } else if (warp >= 24) {
+  } else if (GATE ? warp >= 24 : warp < 16) {
     // ------------------------------------------------------------------ state rows
-    const int k = tid - 768, w4 = warp - 24;
+    const int w4 = warp & 3, k = 32 * w4 + lane;
+    // 8-column pieces of this warp
+    constexpr int kPer = NS == 8 ? 4 : 8;
+    const int qb = NS == 8 ? 4 * ((warp - 8) >> 2) : 0;
     const uint32_t tl = tmem + (uint32_t(32 * w4) << 16);
     const bool mine = k < a.d_k, holds = k < 64 * KB;    // a key column, a row of the copy
     const float* entering = nullptr;
+    if (FULL && a.nseg > 1) wait_for_previous_kernel();    // the state before this piece
     if (FULL)
       entering = a.nseg > 1 ? a.seg_S + (int64_t(rh) * a.nseg + seg) * a.d_v * a.d_k
                             : (a.S_in ? a.S_in + int64_t(rh) * a.d_v * a.d_k : nullptr);
@@ -588,7 +600,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
                        pack2(__uint_as_float(x[6]), __uint_as_float(x[7])));
     };
 #pragma unroll 1
-    for (int q = 0; q < 8; ++q) {
+    for (int q = qb; q < qb + kPer; ++q) {
       uint32_t x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -618,31 +630,28 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       const bool slow = ex > -0.5f;
       const float mul1 = slow ? expm1f(ex) : expf(ex), keep1 = slow ? 1.f : 0.f;
       const uint64_t mul = f2(mul1, mul1), keep = f2(keep1, keep1);
-      ok = warp_wait(&ds_full[i & 1], i >> 1) && (!FULL || warp_wait(y_full, i));
+      ok = warp_wait(ds_full, i) && (!FULL || warp_wait(y_full, i));
       if (!ok) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int q = 0; q < 8; q += 2) {
-        uint32_t d[16], old16[16];
-        tmem_ld16x2(tl + kTD + kNV * (i & 1) + 8 * q, tl + kTS + 8 * q, d, old16);
-        if (q == 6) {
+      for (int q = qb; q < qb + kPer; ++q) {
+        uint32_t d0[8], d1[8], d2[8], old[8], x[8];
+        tmem_ld8x4(tl + kTD + 8 * q, d0, d1, d2, tl + kTS + 8 * q, old);
+        if (q + 1 == qb + kPer) {
           tc_fence_before();
-          warp_arrive(&ds_free[i & 1]);
+          warp_arrive(ds_free);
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint32_t x[8];
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const int b = 8 * u + e;
-            const uint64_t old = u2(old16[b], old16[b + 1]);
-            const float2 n2 = un2(fma2(mul, old, fma2(keep, old, u2(d[b], d[b + 1]))));
-            x[e] = __float_as_uint(n2.x);
-            x[e + 1] = __float_as_uint(n2.y);
-          }
-          tmem_st8(tl + kTS + 8 * (q + u), x);
-          if (FULL) copy8(q + u, x);
+        for (int e = 0; e < 8; e += 2) {
+          const uint64_t own = add2(u2(d0[e], d0[e + 1]),
+                                    add2(u2(d1[e], d1[e + 1]), u2(d2[e], d2[e + 1])));
+          const uint64_t o = u2(old[e], old[e + 1]);
+          const float2 n2 = un2(fma2(mul, o, fma2(keep, o, own)));
+          x[e] = __float_as_uint(n2.x);
+          x[e + 1] = __float_as_uint(n2.y);
         }
+        tmem_st8(tl + kTS + 8 * q, x);
+        if (FULL) copy8(q, x);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -657,7 +666,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       out = a.S_out + int64_t(rh) * a.d_v * a.d_k;
     if (out) {
 #pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
+      for (int q = qb / 2; q < (qb + kPer) / 2; ++q) {
         float x[16];
         tmem_ld16(tl + kTS + 16 * q, x);
 #pragma unroll
@@ -665,12 +674,14 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
           if (mine && 16 * q + e < nv) out[int64_t(v0 + 16 * q + e) * a.d_k + k] = x[e];
       }
     }
-    if (!FULL && tile == 0 && k == 0)
+    if (!FULL && tile == 0 && k == 0 && qb == 0)
       a.seg_a[int64_t(rh) * a.nseg + seg] = float(exp2(logsum));
   } else {
     // ------------------------------------------------------------------ outputs
     if (FULL) {
-      const int w4 = warp & 3, t = 32 * w4 + lane, hf = (warp - 8) >> 2;
+      const int w4 = warp & 3, t = 32 * w4 + lane;
+      constexpr int kPer = NY == 8 ? 2 : 4;             // 16-column pieces of this warp
+      const int hb = NY == 8 ? 2 * ((warp - 8) >> 2) : 0;
       const uint32_t tl = tmem + (uint32_t(32 * w4) << 16);
       const int v0 = kNV * tile, nv = min(kNV, a.d_v - v0);
       const bool skip = a.D != nullptr;
@@ -691,7 +702,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         if (GATE && live) {
           // the row's four sectors on their way to L1 while the products run
 #pragma unroll
-          for (int q = 2 * hf; q < 2 * hf + 2; ++q)
+          for (int q = hb; q < hb + kPer; ++q)
             if (16 * q < nv) asm volatile("prefetch.global.L1 [%0];" ::"l"(zrow + 2 * q));
         }
         ok = warp_wait(&sc_full[s], i / NST);
@@ -708,7 +719,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
-        for (int hq = 2 * hf; hq < 2 * hf + 2; ++hq) {   // 16 columns, two 16-byte pieces of a row
+        for (int hq = hb; hq < hb + kPer; ++hq) {   // 16 columns, two 16-byte pieces of a row
           uint4 z4[2], v4[2];
           unsigned char* at[2];
 #pragma unroll
@@ -825,10 +836,10 @@ cudaError_t run(const ChunkScan& c, cudaStream_t st) {
     if ((e = launch_scan_join(c.a, st)) != cudaSuccess) return e;
   }
   const unsigned grid = unsigned(chains * c.a.nseg);
-  if (c.a.z)
-    scan_chunk_kernel<KB, true, true><<<grid, kThr, bytes, st>>>(c);
-  else
-    scan_chunk_kernel<KB, true, false><<<grid, kThr, bytes, st>>>(c);
+  auto full = c.a.z ? scan_chunk_kernel<KB, true, true> : scan_chunk_kernel<KB, true, false>;
+  // the outputs of a piece can start before its entering state is there
+  if (c.a.nseg > 1) return launch_dependent(full, grid, kThr, bytes, st, c);
+  full<<<grid, kThr, bytes, st>>>(c);
   return cudaGetLastError();
 }
 
