@@ -20,11 +20,10 @@
 // One block per (sequence, head, 64 value columns, piece), one per SM:
 //   warps 0-7    G -> P (thread = token t, half of the columns; P into tensor memory as the A
 //                operand of Y1); warps 0-3 also the next chunk's scalars (dt, running sums)
-//   outputs (thread = token t): Y1 + e^{c_t} Y2, D, gate; y staged over v (rows of 32 scattered
-//                16-byte stores would take half of the data pipe)
-//   state rows (thread = key column, S^T in tensor memory): S = e^{c_C} S + dS and its bf16 copy
-//                these two share warps 8-15, half of the columns each, and 24-27: a gate makes the
-//                outputs the longer work, without one the state's chain is
+//   warps 8-15   outputs (thread = token t, half of the columns): Y1 + e^{c_t} Y2, D, gate; y staged
+//                over v (rows of 32 scattered 16-byte stores would take half of the data pipe)
+//   warps 24-27  state rows (thread = key column, S^T in tensor memory): S = e^{c_C} S + dS and its
+//                bf16 copy. In the first run of a piece, which has no outputs: warps 8-15
 //   warps 16-23  W V (thread = token s, half of the columns)
 //   warp 28      tcgen05.mma: dS;   warp 29  tcgen05.mma: Y1, the next chunk's G, Y2
 //   warp 30      TMA loads of v, stores of y
@@ -184,7 +183,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   uint32_t* holder = reinterpret_cast<uint32_t*>(sm + Y::kSc);
   const ScanArgs& a = c.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int NY = GATE ? 8 : 4, NS = 12 - NY;       // output and state warps
+  constexpr int NY = FULL ? 8 : 4, NS = 12 - NY;       // output and state warps
 
   // block -> (sequence, head, value columns, piece); neighbours share keys and queries
   const int nseg = FULL ? a.nseg : a.nseg - 1;
@@ -576,7 +575,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       }
     }
     if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 63, 0);
-  } else if (GATE ? warp >= 24 : warp < 16) {
+  } else if (FULL ? warp >= 24 : warp < 16) {
     // ------------------------------------------------------------------ state rows
     const int w4 = warp & 3, k = 32 * w4 + lane;
     // 8-column pieces of this warp
