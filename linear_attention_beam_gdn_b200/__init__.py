@@ -258,9 +258,15 @@ def ola_scan_step(desc: ScanDesc, Bp, v, dt, A, k, q, D, dt_bias, z, state_in, p
 
 # ------------------------------------------------------------------ torch-facing wrappers
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _stream_ptr(stream=None) -> int:
@@ -452,28 +458,42 @@ class _Scope:
 
     def __init__(self, index, stream):
         torch = _torch()
-        self.index = index
-        self.device = self.stream = None
-        if torch._C._cuda_getDevice() != index:
-            self.device = torch.cuda.device(index)
-        if stream is not None:
-            self.stream = torch.cuda.stream(stream)
-        self.raw = stream.cuda_stream if stream is not None else None
+        self.index, self.stream = index, stream
+        self.device = torch.cuda.device(index)
+        self.on = torch.cuda.stream(stream) if stream is not None else None
 
     def __enter__(self):
-        if self.device is not None:
-            self.device.__enter__()
-        if self.stream is not None:
-            self.stream.__enter__()
-        else:
-            self.raw = _torch()._C._cuda_getCurrentRawStream(self.index)
+        self.device.__enter__()
+        if self.on is None:
+            return _torch()._C._cuda_getCurrentRawStream(self.index)
+        self.on.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.on is not None:
+            self.on.__exit__(*exc)
+        self.device.__exit__(*exc)
+
+
+class _Here:
+    """The same for a call on the current device and stream."""
+    __slots__ = ("raw",)
+
+    def __init__(self, raw):
+        self.raw = raw
+
+    def __enter__(self):
         return self.raw
 
     def __exit__(self, *exc):
-        if self.stream is not None:
-            self.stream.__exit__(*exc)
-        if self.device is not None:
-            self.device.__exit__(*exc)
+        pass
+
+
+def _scope(index, stream):
+    c = _torch()._C
+    if stream is None and c._cuda_getDevice() == index:
+        return _Here(c._cuda_getCurrentRawStream(index))
+    return _Scope(index, stream)
 
 
 def _first(x, name, ndim):
@@ -506,7 +526,7 @@ def _bad(x, name, shape, dtype, index):
 def _ptr(x, name, shape, dtype, index):
     """Pointer of a contiguous tensor argument."""
     try:
-        if (x.shape == shape and x.dtype == dtype and x.is_cuda and x.get_device() == index and
+        if (x.shape == shape and x.dtype is dtype and x.get_device() == index and
                 x.is_contiguous()):
             return x.data_ptr()
     except AttributeError:
@@ -522,7 +542,7 @@ def _rows(x, name, shape, dtype, index):
     """(pointer, token stride, sequence stride) of a [sequence, token, ...] argument whose channels
     are contiguous; strides of 0 stand for a contiguous tensor."""
     try:
-        fine = x.shape == shape and x.dtype == dtype and x.is_cuda and x.get_device() == index
+        fine = x.shape == shape and x.dtype is dtype and x.get_device() == index
     except AttributeError:
         fine = False
     if not fine:
@@ -573,7 +593,7 @@ def conv(x, w, bias=None, *, state=None, lens=None, silu=True, out=None, state_o
     ix, code = _first(x, "x", 3)
     R, P, C = shape = x.shape
     W, dt, f32 = _taps(w), x.dtype, torch.float32
-    with _Scope(ix, stream) as st:
+    with _scope(ix, stream) as st:
         if out is None:
             out = torch.empty(shape, device=x.device, dtype=dt)
         win = (R, W - 1, C)
@@ -602,7 +622,7 @@ def conv_step(x, w, bias=None, *, state, parent_idx=None, silu=True, out=None, s
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise ValueError("state must be a tensor [R, Bp, W-1, C]")
     Bp = state.shape[1]
-    with _Scope(ix, stream) as st:
+    with _scope(ix, stream) as st:
         if out is None:
             out = torch.empty(shape, device=x.device, dtype=dt)
         if state_out is None:
@@ -648,7 +668,7 @@ def qk_norm(q, k, *, wq=None, wk=None, eps=1e-6, l2=False, positions=None, inv_f
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
     half = inv_freq.numel() if inv_freq is not None else 0
-    with _Scope(ix, stream) as st:
+    with _scope(ix, stream) as st:
         if q_out is None:
             q_out = torch.empty(qs, device=q.device, dtype=dt)
         if k_out is None:
@@ -700,7 +720,7 @@ def scan(v, dt, A, k, q, *, D=None, dt_bias=None, z=None, S_in=None, lens=None, 
     torch = _torch()
     ix, code = _first(v, "v", 4)
     R, P, H, d_v = vs = v.shape
-    with _Scope(ix, stream) as st:
+    with _scope(ix, stream) as st:
         if out is None:
             out = torch.empty(vs, device=v.device, dtype=v.dtype)
         desc, ptrs, yp = _scan_args(v, dt, A, k, q, D, dt_bias, z, out, softplus, ix, code)
@@ -733,7 +753,7 @@ def scan_step(v, dt, A, k, q, *, state, D=None, dt_bias=None, z=None, parent_idx
     if not isinstance(state, torch.Tensor) or state.dim() != 5:
         raise ValueError("state must be a tensor [R, Bp, H, d_v, d_k]")
     Bp = state.shape[1]
-    with _Scope(ix, stream) as st:
+    with _scope(ix, stream) as st:
         if out is None:
             out = torch.empty(vs, device=v.device, dtype=v.dtype)
         desc, ptrs, yp = _scan_args(v, dt, A, k, q, D, dt_bias, z, out, softplus, ix, code)
