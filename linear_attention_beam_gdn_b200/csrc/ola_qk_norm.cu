@@ -61,6 +61,10 @@ __global__ void __launch_bounds__(kQkThreads, qk_blocks(NI, ROT)) qk_norm_kernel
   const int uq = (a.Hq + NG - 1) / NG, uk = (a.Hk + NG - 1) / NG;   // head groups
   const int per = (uq + uk + a.hsplit - 1) / a.hsplit;
   const float inv_d = 1.f / float(a.d);
+  auto freq = [&](int f) -> double {              // turns per position
+    return double(__ldg(a.inv_freq + f)) * 0.15915494309189533577;
+  };
+  const double first = ROT && lane < a.rot / 2 ? freq(lane) : 0.0;
   for (int64_t w = w0; w < a.N * a.hsplit; w += nwarp) {
     const int64_t tok = w / a.hsplit;
     const int part = int(w - tok * a.hsplit);
@@ -96,9 +100,16 @@ __global__ void __launch_bounds__(kQkThreads, qk_blocks(NI, ROT)) qk_norm_kernel
       for (int f = lane; f < nang; f += 32) {
         float c = 1.f, s = 0.f;
         if (f < a.rot / 2) {
-          double turns = pos * double(__ldg(a.inv_freq + f)) * 0.15915494309189533577;
+          double turns = pos * (f < 32 ? first : freq(f));
           turns -= rint(turns);
-          sincospif(float(2.0 * turns), &s, &c);
+          if constexpr (sizeof(T) == 2) {
+            // within 2^-20 in -pi .. pi, far below bf16's 2^-8
+            const float x = float(turns) * 6.283185307179586f;
+            s = __sinf(x);
+            c = __cosf(x);
+          } else {
+            sincospif(float(2.0 * turns), &s, &c);
+          }
         }
         ct[f] = c;
         st[f] = s;
