@@ -32,14 +32,22 @@ __global__ void __launch_bounds__(kQkThreads, qk_blocks(NI, ROT)) qk_norm_kernel
   const int nwarp = gridDim.x * (kQkThreads / 32);
   const int64_t w0 = int64_t(blockIdx.x) * (kQkThreads / 32) + (threadIdx.x >> 5);
   const int nang = ROT ? (a.rot / 2 + 31) / 32 * 32 : 0;   // table entries, filled up
-  float* ct = sm + 2 * a.d + (threadIdx.x >> 5) * 2 * nang;
-  float* st = ct + nang;
   const int nch = a.d / E, half = a.rot / (2 * E), nitem = (nch + 1) / 2;
+  const int nwt = nitem * 2 * E;                  // weights of one kind, filled up
+  float* ct = sm + 2 * nwt + (threadIdx.x >> 5) * 2 * nang;
+  float* st = ct + nang;
+  // the two chunks of item j; the second may lie past the head's end
+  auto chunk0 = [&](int j) { return ROT == 1 && j >= half ? j + half : j; };
+  auto chunk1 = [&](int j) { return ROT == 1 && j < half ? j + half : j + nitem; };
   const bool weighted = a.wq || a.wk;
   if (weighted) {
-    for (int i = threadIdx.x; i < a.d; i += kQkThreads) {
-      sm[i] = a.wq ? __ldg(a.wq + i) : 1.f;
-      sm[a.d + i] = a.wk ? __ldg(a.wk + i) : 1.f;
+    // [four elements of an item][item][4]: neighbouring lanes read neighbouring 16 bytes
+    for (int i = threadIdx.x; i < nwt; i += kQkThreads) {
+      const int four = i / (4 * nitem), j = i / 4 % nitem;
+      const int c = four < E / 4 ? chunk0(j) : chunk1(j);
+      const int ch = c * E + four % (E / 4) * 4 + i % 4;
+      sm[i] = a.wq && c < nch ? __ldg(a.wq + ch) : 1.f;
+      sm[nwt + i] = a.wk && c < nch ? __ldg(a.wk + ch) : 1.f;
     }
     __syncthreads();
   }
@@ -48,15 +56,8 @@ __global__ void __launch_bounds__(kQkThreads, qk_blocks(NI, ROT)) qk_norm_kernel
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int j = gl + i * GL;
-    if (ROT == 1 && j < half) {
-      c0[i] = j;
-      c1[i] = j + half;
-    } else {
-      c0[i] = 2 * j;                              // 2 half + 2 (j - half)
-      c1[i] = 2 * j + 1;
-    }
-    if (j >= nitem) c0[i] = c1[i] = -1;
-    if (c1[i] >= nch) c1[i] = -1;
+    c0[i] = j < nitem ? chunk0(j) : -1;
+    c1[i] = j < nitem && chunk1(j) < nch ? chunk1(j) : -1;
   }
   const int uq = (a.Hq + NG - 1) / NG, uk = (a.Hk + NG - 1) / NG;   // head groups
   const int per = (uq + uk + a.hsplit - 1) / a.hsplit;
@@ -91,8 +92,8 @@ __global__ void __launch_bounds__(kQkThreads, qk_blocks(NI, ROT)) qk_norm_kernel
       }
     };
     fetch(u0);
-    // cos, sin of an item's E angles: E pairs of chunks (j, j + half), or E / 2 pairs inside each
-    // of the two chunks; item j holds the angles j E .. j E + E - 1 in both
+    // cos, sin of an item's E angles: of the pairs of chunks (j, j + half), or of E / 2 pairs
+    // inside each of its two chunks
     uint64_t cs[NI][H2], sn[NI][H2];
     if (ROT) {
       __syncwarp();
@@ -117,18 +118,15 @@ __global__ void __launch_bounds__(kQkThreads, qk_blocks(NI, ROT)) qk_norm_kernel
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int f = (gl + i * GL) * E;
+        const int j = gl + i * GL;
 #pragma unroll
-        for (int e = 0; e < H2; e += 2) {
-          ulonglong2 c2 = make_ulonglong2(0, 0), s2 = c2;
-          if (f < nang) {
-            c2 = *reinterpret_cast<const ulonglong2*>(ct + f + 2 * e);
-            s2 = *reinterpret_cast<const ulonglong2*>(st + f + 2 * e);
-          }
-          cs[i][e] = c2.x;
-          sn[i][e] = s2.x;
-          cs[i][e + 1] = c2.y;
-          sn[i][e + 1] = s2.y;
+        for (int e = 0; e < H2; ++e) {
+          // ROT 2: pairs 0 .. H2 / 2 - 1 belong to chunk j, the others to chunk j + nitem
+          const int f = ROT == 1          ? j * E + 2 * e
+                        : 2 * e < H2      ? j * H2 + 2 * e
+                                          : (j + nitem) * H2 + 2 * e - H2;
+          cs[i][e] = f < nang ? *reinterpret_cast<const uint64_t*>(ct + f) : 0;
+          sn[i][e] = f < nang ? *reinterpret_cast<const uint64_t*>(st + f) : 0;
         }
       }
     }
@@ -159,11 +157,10 @@ __global__ void __launch_bounds__(kQkThreads, qk_blocks(NI, ROT)) qk_norm_kernel
       const float rs = rsqrtf((a.l2 ? s : s * inv_d) + a.eps);
       if (!on) continue;
       const uint64_t rs2 = f2(rs, rs);
-      const float* wt = sm + (isq ? 0 : a.d);
+      const float* wt = sm + (isq ? 0 : nwt) + 4 * gl;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         if (c0[i] < 0) continue;
-        const int d1 = c1[i] < 0 ? c0[i] : c1[i];
 #pragma unroll
         for (int e = 0; e < H2; ++e) {
           x0[i][e] = mul2(x0[i][e], rs2);
@@ -172,8 +169,9 @@ __global__ void __launch_bounds__(kQkThreads, qk_blocks(NI, ROT)) qk_norm_kernel
         if (weighted) {
 #pragma unroll
           for (int e = 0; e < H2; e += 2) {
-            const ulonglong2 a2 = *reinterpret_cast<const ulonglong2*>(wt + c0[i] * E + 2 * e);
-            const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(wt + d1 * E + 2 * e);
+            const float* p = wt + 4 * (i * GL + e / 2 * nitem);
+            const ulonglong2 a2 = *reinterpret_cast<const ulonglong2*>(p);
+            const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(p + nwt / 2);
             x0[i][e] = mul2(x0[i][e], a2.x);
             x0[i][e + 1] = mul2(x0[i][e + 1], a2.y);
             x1[i][e] = mul2(x1[i][e], b2.x);
@@ -233,7 +231,9 @@ __global__ void __launch_bounds__(kQkThreads, qk_blocks(NI, ROT)) qk_norm_kernel
 template <typename T, int GL, int NI>
 cudaError_t run(const QkArgs& a, int pair, unsigned grid, cudaStream_t st) {
   const int nang = a.rot ? (a.rot / 2 + 31) / 32 * 32 : 0;
-  const size_t smem = sizeof(float) * 2 * (a.d + nang * (kQkThreads / 32));
+  constexpr int E = 16 / int(sizeof(T));
+  const int nwt = (a.d / E + 1) / 2 * 2 * E;
+  const size_t smem = sizeof(float) * 2 * (nwt + nang * (kQkThreads / 32));
   if (!a.rot)
     qk_norm_kernel<T, GL, NI, 0><<<grid, kQkThreads, smem, st>>>(a);
   else if (pair)
