@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanArgs a) {
       s.w = fmaf(al, s.w, w * kk[j].w);
       o[u] = fmaf(s.x, qq[j].x, fmaf(s.y, qq[j].y, fmaf(s.z, qq[j].z, fmaf(s.w, qq[j].w, o[u]))));
       if (row < a.d_v)
-        *reinterpret_cast<float4*>(dst + int64_t(row) * DK + (j * TPR + lt) * 4) = s;
+        __stcs(reinterpret_cast<float4*>(dst + int64_t(row) * DK + (j * TPR + lt) * 4), s);
     }
   }
   auto finish = [&](int u, float x) {
