@@ -62,8 +62,9 @@ struct Lay {
   static constexpr uint32_t kSc = kS + KB * 8192;          // scalars per stage
   static constexpr uint32_t kBar = kSc + NST * kScFloats * 4;
   static constexpr int kNBar = 7 * NST + 12;
+  static constexpr uint32_t kBad = kBar + kNBar * 8;       // flag
   // the tensor-memory address is handed over in the scalars' place, before they are written
-  static constexpr uint32_t kBytes = kBar + kNBar * 8;
+  static constexpr uint32_t kBytes = kBad + 8;
 };
 static_assert(Lay<1>::kBar % 8 == 0 && Lay<2>::kBar % 8 == 0, "mbarriers");
 static_assert(Lay<1>::kBytes <= 232448 && Lay<2>::kBytes <= 232448, "shared memory per block");
@@ -156,6 +157,57 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
+// A value that is not finite makes NaN of its products with the masked weights too, so of its
+// column's outputs earlier in its chunk. They are taken again, token by token from the piece's
+// start; a warp per column. From the value on the column's outputs and state are not finite anyway.
+__device__ __noinline__ void redo_column(const ScanArgs& a, const float* entering, int r, int h,
+                                         int g, int col, int p0, int p1) {
+  const int lane = threadIdx.x & 31;
+  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + int64_t(r) * a.v_seq +
+                           int64_t(h) * a.d_v + col;
+  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + int64_t(r) * a.k_seq +
+                           int64_t(g) * a.d_k;
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + int64_t(r) * a.q_seq +
+                           int64_t(g) * a.d_k;
+  int first = p1;
+  for (int b = p0; b < p1 && first == p1; b += 32) {
+    const int p = b + lane;
+    const bool odd = p < p1 && !(fabsf(to_f32(v[int64_t(p) * a.v_tok])) < INFINITY);
+    const uint32_t m = __ballot_sync(kFull, odd);
+    if (m) first = b + __ffs(m) - 1;
+  }
+  if (first == p1) return;
+  const int chunk = p0 + (first - p0) / kQ * kQ;
+  float S[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = lane + 32 * j;
+    S[j] = entering && e < a.d_k ? entering[int64_t(col) * a.d_k + e] : 0.f;
+  }
+  for (int p = p0; p < first; ++p) {
+    float dt = a.dt[(int64_t(r) * a.P + p) * a.H + h] + (a.dt_bias ? a.dt_bias[h] : 0.f);
+    if (a.softplus) dt = softplus_f(dt);
+    const float al = expf(dt * a.A[h]), vp = to_f32(v[int64_t(p) * a.v_tok]), w = dt * vp;
+    float o = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = lane + 32 * j;
+      if (e >= a.d_k) break;
+      S[j] = fmaf(al, S[j], w * to_f32(k[int64_t(p) * a.k_tok + e]));
+      if (p >= chunk) o = fmaf(S[j], to_f32(q[int64_t(p) * a.q_tok + e]), o);
+    }
+    if (p < chunk) continue;
+    o = group_sum(o, 32);
+    if (a.D) o = fmaf(a.D[h], vp, o);
+    if (a.z)
+      o *= silu_f<__nv_bfloat16>(to_f32(static_cast<const __nv_bfloat16*>(
+          a.z)[int64_t(r) * a.z_seq + int64_t(p) * a.z_tok + int64_t(h) * a.d_v + col]));
+    if (lane == 0)
+      static_cast<__nv_bfloat16*>(a.y)[int64_t(r) * a.y_seq + int64_t(p) * a.y_tok +
+                                       int64_t(h) * a.d_v + col] = from_f32<__nv_bfloat16>(o);
+  }
+}
+
 template <int KB, bool FULL, bool GATE>
 __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_constant__ ChunkScan c) {
   using Y = Lay<KB>;
@@ -180,6 +232,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   uint64_t* y_full = one + 9;            // Y1 and Y2 done
   uint64_t* y_free = one + 10;           // Y1 and Y2 read (NY warps)
   uint64_t* done = one + 11;             // every MMA completed (both issuers)
+  volatile uint32_t* bad = reinterpret_cast<uint32_t*>(sm + Y::kBad);   // a state is not finite
   uint32_t* holder = reinterpret_cast<uint32_t*>(sm + Y::kSc);
   const ScanArgs& a = c.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -195,6 +248,18 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   const int64_t pb = int64_t(seg) * a.seg_len;
   const int p0 = int(pb < L ? pb : L), p1 = int(pb + a.seg_len < L ? pb + a.seg_len : L);
   const int nch = (p1 - p0 + kQ - 1) / kQ;
+  const int v0 = kNV * tile, nv = min(kNV, a.d_v - v0);
+  float* out =                             // the state behind it
+      !FULL                           ? a.seg_S + (int64_t(rh) * a.nseg + seg) * a.d_v * a.d_k
+      : seg == nseg - 1 && a.S_out ? a.S_out + int64_t(rh) * a.d_v * a.d_k
+                                   : nullptr;
+  // S_out takes S_in's place: written last, since the second look below reads S_in again
+  const bool late = FULL && a.nseg == 1 && a.S_in == a.S_out;
+  const float* entering =                  // the state before the piece
+      !FULL        ? nullptr
+      : a.nseg > 1 ? a.seg_S + (int64_t(rh) * a.nseg + seg) * a.d_v * a.d_k
+      : a.S_in     ? a.S_in + int64_t(rh) * a.d_v * a.d_k
+                   : nullptr;
 
   if (smem_u32(sm) & 1023u) {              // the swizzled tiles' alignment; the whole block leaves
     if (tid == 0) report_error(a.err, OLA_ERR_CUDA, 59, 0);
@@ -222,6 +287,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
     mbar_init(y_full, 1);
     mbar_init(y_free, NY);
     mbar_init(done, 2);
+    *bad = 0;
     fence_barrier_init();
   }
   if (warp == 29) tmem_alloc(holder, 512);
@@ -416,6 +482,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       // tokens behind the end take no part: dt = 0
       float dt = raw + bias;
       if (a.softplus) dt = softplus_f(dt);
+      if (A2 != A2) dt = A2;                 // the clamp below would hide it
       if (t >= p1 - (p0 + i * kQ)) dt = 0.f;
       raw = load_dt(i + 1);
       // a decay below 2^-256 is 0; the clamp keeps sums of resets finite
@@ -583,12 +650,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
     const int qb = NS == 8 ? 4 * ((warp - 8) >> 2) : 0;
     const uint32_t tl = tmem + (uint32_t(32 * w4) << 16);
     const bool mine = k < a.d_k, holds = k < 64 * KB;    // a key column, a row of the copy
-    const float* entering = nullptr;
     if (FULL && a.nseg > 1) wait_for_previous_kernel();    // the state before this piece
-    if (FULL)
-      entering = a.nseg > 1 ? a.seg_S + (int64_t(rh) * a.nseg + seg) * a.d_v * a.d_k
-                            : (a.S_in ? a.S_in + int64_t(rh) * a.d_v * a.d_k : nullptr);
-    const int v0 = kNV * tile, nv = min(kNV, a.d_v - v0);
     unsigned char* row = sm + Y::kS + k * 128;             // the copy: 64 columns, 128-byte swizzle
     auto copy8 = [&](int q, const uint32_t (&x)[8]) {
       if (holds)
@@ -658,20 +720,25 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       warp_arrive(s_full);
     }
     if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 64, 0);
-    float* out = nullptr;
-    if (!FULL)
-      out = a.seg_S + (int64_t(rh) * a.nseg + seg) * a.d_v * a.d_k;
-    else if (seg == nseg - 1 && a.S_out)
-      out = a.S_out + int64_t(rh) * a.d_v * a.d_k;
-    if (out) {
+    if (out || FULL) {
+      uint64_t odd = f2(0.f, 0.f);           // NaN once an element is not finite
 #pragma unroll 1
       for (int q = qb / 2; q < (qb + kPer) / 2; ++q) {
         float x[16];
         tmem_ld16(tl + kTS + 16 * q, x);
+        if (out && !late) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (mine && 16 * q + e < nv) out[int64_t(v0 + 16 * q + e) * a.d_k + k] = x[e];
+          for (int e = 0; e < 16; ++e)
+            if (mine && 16 * q + e < nv) out[int64_t(v0 + 16 * q + e) * a.d_k + k] = x[e];
+        }
+        if (FULL) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) odd = fma2(f2(x[e], x[e + 1]), f2(0.f, 0.f), odd);
+        }
       }
+      const float2 o2 = un2(odd);
+      if (FULL && mine && o2.x + o2.y != 0.f) *bad = 1;
+      __syncwarp();
     }
     if (!FULL && tile == 0 && k == 0 && qb == 0)
       a.seg_a[int64_t(rh) * a.nseg + seg] = float(exp2(logsum));
@@ -682,7 +749,6 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       constexpr int kPer = NY == 8 ? 2 : 4;             // 16-column pieces of this warp
       const int hb = NY == 8 ? 2 * ((warp - 8) >> 2) : 0;
       const uint32_t tl = tmem + (uint32_t(32 * w4) << 16);
-      const int v0 = kNV * tile, nv = min(kNV, a.d_v - v0);
       const bool skip = a.D != nullptr;
       const float D = skip ? a.D[h] : 0.f;
       const uint64_t D2 = f2(D, D);
@@ -765,6 +831,26 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
         warp_arrive(&v_done[s]);
       }
       if (!ok && lane == 0) report_error(a.err, OLA_ERR_TIMEOUT, 65, 0);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (FULL && *bad) {
+    // every output has been stored by now
+    for (int col = warp; col < nv; col += kThr / 32)
+      redo_column(a, entering, r, h, g, v0 + col, p0, p1);
+    __syncthreads();
+  }
+  if (late && out && warp >= 24 && warp < 28) {
+    const int w4 = warp & 3, k = 32 * w4 + lane;
+#pragma unroll 1
+    for (int q = 0; q < kNV / 16; ++q) {
+      float x[16];
+      tmem_ld16(tmem + (uint32_t(32 * w4) << 16) + kTS + 16 * q, x);
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (k < a.d_k && 16 * q + e < nv) out[int64_t(v0 + 16 * q + e) * a.d_k + k] = x[e];
     }
   }
   tc_fence_before();

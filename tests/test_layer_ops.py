@@ -203,6 +203,19 @@ def test_scan_refuses_pointers(L):
     assert L.ola_scan(ctypes.byref(d), *far, far[0], n, None) == 1
 
 
+def test_refuses_lengths_past_the_limit(L):
+    """A sequence of more than 2^30 tokens (or that many beams) is unsupported, not wrapped."""
+    n = (1 << 30) + 1
+    far = [(i + 1) << 50 for i in range(12)]
+    c = _conv_desc(R=1, P=n, C=8)
+    assert L.ola_conv(ctypes.byref(c), *far[:7], None) == 2
+    assert L.ola_conv_step(ctypes.byref(c), 1, *far[:4], None, *far[5:7], None) == 2
+    d = _scan_desc(R=1, P=n, H=1, G=1, d_k=16, d_v=16)
+    assert L.ola_scan(ctypes.byref(d), *far, None, 0, None) == 2
+    assert L.ola_scan_step(ctypes.byref(d), 1, *far, None) == 2
+    assert L.ola_scan_workspace_bytes(ctypes.byref(d), ctypes.byref(ctypes.c_uint64())) == 2
+
+
 def test_wrappers_refuse_tensors(L):
     x, w = torch.zeros(1, 4, 8), torch.zeros(8, 4)
     with pytest.raises(ValueError):
@@ -542,6 +555,68 @@ def test_scan_decays_of_every_size(dtype):
     y, S = ola.scan(**{n: t.cuda() for n, t in c.items()}, S_in=cu(o["S_in"]), softplus=False)
     close(y, y64, ty, "y")
     close(S, S64, tS, "state")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dk,z", [(64, False), (64, True), (128, False), (128, True)])
+def test_scan_many_chunks_in_one_piece(dk, z):
+    """So many heads that no sequence is cut: every stage of the chunk pipeline is used again and
+    again, by heads that end at different chunks."""
+    R, P, H, dv = 2, 900, 40, 32
+    lens = [900, 641]
+    c, o = _scan_case(BF, R, P, H, 1, dk, dv, z=z, D=True, state=True, lens=lens, seed=3)
+    out0 = torch.full((R, P, H, dv), 3.0, dtype=BF)
+    y64, S64, ty, tS = ref.scan(**c, D=o["D"], dt_bias=o["dt_bias"], z=o["z"], S_in=o["S_in"],
+                                lens=o["lens"], use_softplus=True, out0=out0, chunked=True)
+    cg = {n: t.cuda() for n, t in c.items()}
+    first = None
+    for _ in range(3):
+        y, S = ola.scan(**cg, D=cu(o["D"]), dt_bias=cu(o["dt_bias"]), z=cu(o["z"]),
+                        S_in=cu(o["S_in"]), lens=cu(o["lens"]), out=out0.cuda())
+        assert ola.layer_status() == ola.OLA_OK
+        if first is None:
+            close(y, y64, ty, "y")
+            close(S, S64, tS, "state")
+            first = y, S
+        same(y, first[0], "y")
+        same(S, first[1], "state")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,H,dk,z,lens", [
+    (BF, 2, 128, True, None), (BF, 2, 64, False, [300, 270]), (BF, 2, 32, True, [300, 270]),
+    (BF, 40, 16, False, None), (BF, 40, 128, True, [300, 270]), (F, 2, 32, True, None)])
+def test_scan_values_that_are_not_finite_stay_causal(dtype, H, dk, z, lens):
+    """An infinity or NaN in v reaches its own column, from its own token on, and nothing else."""
+    R, P, dv = 2, 300, 64
+    c, o = _scan_case(dtype, R, P, H, 1, dk, dv, z=z, D=True, state=True, lens=lens, seed=4)
+    c["v"][:, 5::7] = -0.0                               # an ordinary value, also beside the others
+    bad = [(0, 10, 0, 63, NAN), (0, 140, 1, 5, float("inf")), (0, 200, 1, 5, -float("inf")),
+           (1, 127, 0, 0, -float("inf")), (1, 128, 0, 1, NAN), (1, 255, 1, 33, float("inf")),
+           (1, 269, 1, 34, NAN), (1, 160, 1, 31, NAN)]
+    dirty = c["v"].clone()
+    hit = torch.zeros(R, P, H, dv, dtype=torch.bool)
+    for r, p, h, e, x in bad:
+        c["v"][r, p, h, e], dirty[r, p, h, e] = 0.0, x
+        hit[r, p:P if lens is None else lens[r], h, e] = True
+    out0 = torch.full((R, P, H, dv), 3.0, dtype=dtype)
+    y64, S64, ty, tS = ref.scan(**c, D=o["D"], dt_bias=o["dt_bias"], z=o["z"], S_in=o["S_in"],
+                                lens=o["lens"], use_softplus=True, out0=out0,
+                                chunked=_chunked(dtype, dk))
+    kw = {n: t.cuda() for n, t in c.items() if n != "v"}
+    rows = hit.any(1)                                     # [R, H, dv]
+    for in_place in (False, True):
+        S_in = cu(o["S_in"])
+        y, S = ola.scan(dirty.cuda(), **kw, D=cu(o["D"]), dt_bias=cu(o["dt_bias"]), z=cu(o["z"]),
+                        S_in=S_in, S_out=S_in if in_place else None, lens=cu(o["lens"]),
+                        out=out0.cuda())
+        assert ola.layer_status() == ola.OLA_OK
+        y, S = y.cpu(), S.cpu()
+        assert not torch.isfinite(y[hit]).any()
+        close(y.masked_fill(hit, 0.0), y64.masked_fill(hit, 0.0), ty, "y elsewhere")
+        assert not torch.isfinite(S[rows]).any()
+        close(S.masked_fill(rows[..., None], 0.0), S64.masked_fill(rows[..., None], 0.0), tS,
+              "state elsewhere")
 
 
 @pytest.mark.gpu
