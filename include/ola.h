@@ -274,7 +274,8 @@ ola_status ola_decode_noalloc(const ola_geometry* geom, const float* S_ctx, cons
  * - Device-side errors (a bad parent, a bounded wait that ran out) go to one sticky word per
  *   device; the call carries on. ola_layer_status reads and clears it.
  * - Pointers to q, k, v, x, y, z and states: aligned to their element; 16-byte aligned pointers and
- *   rows (strides) run on wide accesses and on tensor memory copies. fp32 pointers: 4 bytes. */
+ *   rows (strides) run on wide accesses and TMA copies. fp32 pointers: 4 bytes.
+ * - Forward only, like every operator of the library: nothing is kept for gradients. */
 
 /* Wait for `stream`, return the first device-side error that a call of this section recorded on
  * the current device since the last ola_layer_status (OLA_OK if none), and clear it. Not to be
@@ -347,8 +348,9 @@ ola_status ola_qk_norm(const ola_qk_desc* d, const void* q, const void* k, const
  *   S_in    : [R][H][d_v][d_k] fp32 or NULL;  S_out : the same, or NULL; may be S_in itself
  *   ws      : device scratch of ola_scan_workspace_bytes(d) bytes, 16-byte aligned (NULL if 0).
  *             Calls that may overlap on the GPU need scratch of their own.
- * d_k, d_v in {16, 32, 64, 128, 256}, G divides H, R * H <= 2^24, P 0..2^30. dt * A is taken to be <= 0 (a decay);
- * growth is computed as the formula says as long as it does not overflow. States and sums are
+ * d_k, d_v in {16, 32, 64, 128, 256}, G divides H, R * H <= 2^24, P 0..2^30. dt * A is taken to
+ * be <= 0 (a decay); growth is computed as the formula says as long as it does not overflow. A NaN
+ * or infinity reaches what the formula makes of it and no earlier token, row or column. States and sums are
  * fp32. bf16 prompts with 16-byte aligned rows and d_k <= 128 run in chunks of 128 tokens on
  * tensor cores: keys, queries and v enter exactly; the token-to-token weights and the copy of
  * the state that meets the queries are rounded to bf16 on the way to y (y itself is bf16), the

@@ -9,6 +9,13 @@
 // in once, transposed through shared memory ([tap][channel], read 16 bytes at a time); sums run two
 // channels per instruction. The window's values are moved, never recomputed: the state that leaves
 // is the input's bits.
+//
+// Loads run through a ring in shared memory that each thread fills for itself (cp.async): deep
+// prefetch without registers or barriers. Measured: 8 x 5120 tokens of 6144 bf16 channels in 177 us
+// (1.0 GB, 87 % of the copy rate; 8-byte vectors 270 us, 16-byte ones without the ring 244 us);
+// 8192 beams in 112 us (91 %; without the ring 135 us). One prompt of 1024 tokens takes 9.6 us
+// where the copy rate gives 3.9: launch, taps and the ring's first fill. Rows whose start or
+// stride is not a multiple of 16 bytes go one channel per thread.
 #include <type_traits>
 
 #include "ola_layer.cuh"
@@ -355,7 +362,10 @@ cudaError_t launch(ConvArgs a, int in_dtype, int W, bool wide, bool step, cudaSt
   while (bx < 32 && bx < nvec) bx *= 2;
   const int by = kConvThreads / bx;
   a.n_ctile = int((nvec + bx - 1) / bx);
-  // tokens (beams) per thread: as many as leave about 8 blocks for every SM
+  // Tokens (beams) per thread: long stretches share the taps and the window's first reads, short
+  // ones fill the machine. Steps and single channels keep 8 blocks for every SM. Prompts in
+  // vectors keep one: a prompt of 1024 tokens took 12 us at 8 per SM and 10 at 1, since every further
+  // block brings in its taps anew.
   const int64_t rows = step ? int64_t(a.R) * a.P : a.P;
   const int64_t seqs = step ? 1 : a.R;
   a.tt = step ? 8 : 32;

@@ -346,7 +346,7 @@ ola_status ola_scan_workspace_bytes(const ola_scan_desc* d, uint64_t* out_bytes)
   // enough for either form, so that it does not hang on the pointers' alignment
   int n = 1, len = 0;
   const int sms = sm_count();
-  scan_tok_pieces(d->R, d->P, d->H, d->d_k, d->d_v, sms, &n, &len);
+  scan_tok_pieces(d->R, d->P, d->H, d->d_v, sms, &n, &len);
   if (d->in_dtype == OLA_BF16) {
     int n2 = 1;
     scan_chunk_pieces(d->R, d->P, d->H, d->d_v, sms, &n2, &len);
@@ -375,7 +375,7 @@ ola_status ola_scan(const ola_scan_desc* d, const void* v, const float* dt, cons
   if (chunked)
     scan_chunk_pieces(d->R, d->P, d->H, d->d_v, sm_count(), &a.nseg, &a.seg_len);
   else
-    scan_tok_pieces(d->R, d->P, d->H, d->d_k, d->d_v, sm_count(), &a.nseg, &a.seg_len);
+    scan_tok_pieces(d->R, d->P, d->H, d->d_v, sm_count(), &a.nseg, &a.seg_len);
   const uint64_t need = ws_bytes_for(d, a.nseg);
   if (need) {
     if (!ws || ws_bytes < need || !aligned(ws, 16)) return OLA_ERR_INVALID_ARG;

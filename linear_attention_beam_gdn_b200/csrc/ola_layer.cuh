@@ -262,7 +262,7 @@ cudaError_t launch_qk_norm(QkArgs a, int in_dtype, int pair, cudaStream_t stream
 cudaError_t launch_scan_tok(const ScanArgs& a, int in_dtype, cudaStream_t stream);
 cudaError_t launch_scan_join(const ScanArgs& a, cudaStream_t stream);
 cudaError_t launch_scan_step(const ScanArgs& a, int in_dtype, cudaStream_t stream);
-void scan_tok_pieces(int R, int P, int H, int d_k, int d_v, int sms, int* nseg, int* seg_len);
+void scan_tok_pieces(int R, int P, int H, int d_v, int sms, int* nseg, int* seg_len);
 
 bool scan_chunk_supported(const ScanArgs& a, int in_dtype);
 void scan_chunk_pieces(int R, int P, int H, int d_v, int sms, int* nseg, int* seg_len);

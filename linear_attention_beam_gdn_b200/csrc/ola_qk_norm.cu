@@ -7,9 +7,15 @@
 // lane holds items of two 16-byte chunks. An item is one rotation pair of chunks (j, j + rot/2)
 // or two neighbouring chunks, so a rotation never leaves its lane; the sum of squares is joined by
 // shuffles. A warp takes one token's heads 32 / GL at a time, the next ones' loads ahead of the
-// arithmetic, and walks over tokens; weights lie in shared memory. The token's angles are worked out once, one per lane, and handed round
-// through shared memory. Angles are reduced in fp64: position * inv_freq in fp32 would be off by
-// 2^-24 of up to 10^5 radians.
+// arithmetic, and walks over tokens; weights lie in shared memory in the items' order, so that
+// neighbouring lanes read neighbouring 16 bytes. The token's angles are worked out once, one per
+// lane, and handed round through shared memory. Angles are reduced in fp64: position * inv_freq in
+// fp32 would be off by 2^-24 of up to 10^5 radians.
+//
+// Measured, bf16: 40960 tokens of 32 heads of 128 in 105 us (97 % of the copy rate); 20480 tokens of
+// 18 heads of 256, weighted, 64 dims rotated, in 72 us (80 %: the weights' reads and the shuffles
+// share the load-store pipe; with weights in channel order, where lanes met in the banks, it was 85 %
+// busy and took 78 us). Worse: weights in registers (81), loads two groups ahead (81).
 #include "ola_layer.cuh"
 
 namespace ola {
@@ -17,7 +23,8 @@ namespace ola {
 namespace {
 
 constexpr int kQkThreads = 128;
-// resident blocks per SM (the launch bounds): the grid is one such wave, each warp walks on
+// Resident blocks per SM (the launch bounds): the grid is one such wave, each warp walks on. The
+// rotated form takes 71.8 us at 6, 74.2 at 5, 74.9 at 7 and 83 at 8.
 constexpr int qk_blocks(int ni, int rot) { return ni > 1 ? 4 : rot ? 6 : 8; }
 
 // GL lanes per head, NI items per lane (items past the head's end are idle).

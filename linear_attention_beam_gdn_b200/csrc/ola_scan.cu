@@ -6,7 +6,9 @@
 // of them in registers for the whole piece of the sequence, two columns per instruction, and the
 // eight partial sums of o are joined by shuffles, those of four tokens together. Tokens are staged
 // in shared memory 16 at a time as they are, the next tile's copies in flight while one is worked
-// on; what bounds it is the arithmetic, three packed operations per two state elements and token.
+// on; what bounds it is the arithmetic, three packed operations per two state elements and token,
+// and their latency where few blocks run (8 x 792 tokens of 16 heads of 64 x 128 in fp32: 204 us, the
+// operations alone 69 us, the bytes 24).
 //
 // A long prompt of few sequences is cut into pieces: a first pass leaves each piece's own state
 // (from zero) and decay, scan_join_kernel turns these into the state before each piece, and the
@@ -364,7 +366,7 @@ cudaError_t launch_scan_join(const ScanArgs& a, cudaStream_t st) {
 // Pieces: while the sequences alone leave most of the machine idle (fewer than 4 blocks per SM),
 // as many as fill it, of at least 16 tokens each (777 tokens of 18 chains of 64 x 32: 21.6 us, with
 // at least 32 tokens 24.4 us, 64 tokens 29.0 us).
-void scan_tok_pieces(int R, int P, int H, int d_k, int d_v, int sms, int* nseg, int* seg_len) {
+void scan_tok_pieces(int R, int P, int H, int d_v, int sms, int* nseg, int* seg_len) {
   const int64_t chains = int64_t(R) * H * ((d_v + 63) / 64);
   int64_t want = int64_t(4) * sms / chains;
   if (want > P / 16) want = P / 16;
@@ -375,7 +377,6 @@ void scan_tok_pieces(int R, int P, int H, int d_k, int d_v, int sms, int* nseg, 
   *seg_len = int(len);
   *nseg = int((int64_t(P) + len - 1) / len);
   if (*nseg < 1) *nseg = 1;
-  (void)d_k;
 }
 
 cudaError_t launch_scan_tok(const ScanArgs& a, int in_dtype, cudaStream_t st) {

@@ -10,8 +10,9 @@
 //     Y1 = P V                128 x 64 x 128      P = G * decay * dt below the diagonal, as bf16
 //     Y2 = Q S0^T             128 x 64 x d_k      S0 as bf16; o = Y1 + e^{c_t} Y2
 //     dS = K^T (W V)          d_k x 64 x 128      W V in three bf16 parts (24 bits)
-// The state itself stays in fp32 registers and never meets a rounded operand: S_C is as exact as
-// an fp32 sum. P and the copy of S0 are rounded to bf16 on the way to y alone, which is bf16.
+// The state itself stays in fp32 (tensor memory) and never meets a rounded operand: S_C is as exact
+// as an fp32 sum, which is why W V is cut into three bf16 parts and not rounded to one. P and the
+// copy of S0 are rounded to bf16 on the way to y alone, which is bf16 itself.
 //
 // No exponent is ever positive: inside a block of 32 tokens P takes exp2 of the difference of two
 // running sums, between blocks s < t it is (e^{c_t - end of s's block}) (e^{end - c_s} dt_s), a
@@ -22,15 +23,25 @@
 //                operand of Y1); warps 0-3 also the next chunk's scalars (dt, running sums)
 //   warps 8-15   outputs (thread = token t, half of the columns): Y1 + e^{c_t} Y2, D, gate; y staged
 //                over v (rows of 32 scattered 16-byte stores would take half of the data pipe)
+//   warps 16-23  W V (thread = token s, half of the columns)
 //   warps 24-27  state rows (thread = key column, S^T in tensor memory): S = e^{c_C} S + dS and its
 //                bf16 copy. In the first run of a piece, which has no outputs: warps 8-15
-//   warps 16-23  W V (thread = token s, half of the columns)
 //   warp 28      tcgen05.mma: dS;   warp 29  tcgen05.mma: Y1, the next chunk's G, Y2
 //   warp 30      TMA loads of v, stores of y
 //   warp 31      TMA loads of keys and queries
 // Two issuing warps, so that neither chain (G -> P -> Y1 and W V -> dS -> S -> Y2) waits behind the
-// other's operands; nothing but Y2 waits for the state. A piece of a cut sequence runs twice: dS alone first (FULL = false), then, once
-// scan_join_kernel has made the state before every piece, the outputs.
+// other's operands; nothing but Y2 waits for the state. A piece of a cut sequence runs twice: dS
+// alone first (FULL = false), then, once scan_join_kernel has made the state before every piece,
+// the outputs.
+//
+// What bounds it: not HBM (64 prompts of 5120 tokens, 16 heads of 128 x 128: 5.5 GB in 1.57 ms of
+// short runs, 53 % of the copy rate; 46 % in long ones, where the clock falls) and not the matrix
+// pipe (36 % busy), but shared memory: every chunk passes 16 KB of v, y, three parts of W V and the
+// keys and queries through it, most of it twice, and its data pipe is at 70 % with the chains above
+// in front of two stages (64 KB of keys and queries each, three would not fit). Measured and worse:
+// y stored straight from registers (1.74 ms), y staged over the queries (1.90), P in place of G
+// behind barriers of 64 threads (1.74), 16 state columns at a time (1.63), four W V or four output
+// warps (1.85 against 1.79 in long runs).
 #include "ola_layer.cuh"
 
 namespace ola {
@@ -43,7 +54,7 @@ constexpr int kThr = 1024;
 constexpr uint32_t kBlk = kQ * 128;     // 16 KB: 128 rows of 64 bf16 columns
 
 // tensor memory columns
-constexpr uint32_t kTG = 0;             // G, 128; P of 16 tokens (8 columns of bf16 pairs) in their place
+constexpr uint32_t kTG = 0;             // G, 128; then P, 8 columns of bf16 pairs for each 16 of G
 constexpr uint32_t kTD = 128;           // dS of the three parts of W V, 64 each
 constexpr uint32_t kTS = 320;           // S^T fp32, 64
 constexpr uint32_t kTY1 = 384;

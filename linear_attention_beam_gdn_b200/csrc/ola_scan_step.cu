@@ -4,7 +4,10 @@
 //
 // Five operations per state element against 4 bytes read and 4 written: the bound is HBM, and the
 // states are all of it. TPR lanes hold one row of the state as float4; a warp keeps kU rows per
-// lane group in flight, and joins their kU output sums in one folding reduction.
+// lane group in flight, and joins their kU output sums in one folding reduction. New states are
+// written with streaming stores, which leave L2 to the parents that several beams share: 512 beams
+// of 16 heads of 128 x 128 in 145 us (148 without; 89 % of the copy rate over the parents that are
+// read). Heads go fastest over the grid: beams fastest took 167 us.
 #include "ola_layer.cuh"
 
 namespace ola {
