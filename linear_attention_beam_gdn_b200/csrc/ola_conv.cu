@@ -11,10 +11,10 @@
 // is the input's bits.
 //
 // Loads run through a ring in shared memory that each thread fills for itself (cp.async): deep
-// prefetch without registers or barriers. Measured: 8 x 5120 tokens of 6144 bf16 channels in 177 us
-// (1.0 GB, 87 % of the copy rate; 8-byte vectors 270 us, 16-byte ones without the ring 244 us);
-// 8192 beams in 112 us (91 %; without the ring 135 us). One prompt of 1024 tokens takes 9.6 us
-// where the copy rate gives 3.9: launch, taps and the ring's first fill. Rows whose start or
+// prefetch without registers or barriers. Measured: 8 x 5120 tokens of 6144 bf16 channels in 167 us
+// (1.0 GB, 92 % of the copy rate; before the ring 244 us, with 8-byte vectors 270); 8192 beams in
+// 112 us (91 %; without the ring 135 us). One prompt of 1024 tokens takes 8.3 us where the copy
+// rate gives 3.9: launch, taps and the ring's first fill. Rows whose start or
 // stride is not a multiple of 16 bytes go one channel per thread.
 #include <type_traits>
 
@@ -362,20 +362,26 @@ cudaError_t launch(ConvArgs a, int in_dtype, int W, bool wide, bool step, cudaSt
   while (bx < 32 && bx < nvec) bx *= 2;
   const int by = kConvThreads / bx;
   a.n_ctile = int((nvec + bx - 1) / bx);
-  // Tokens (beams) per thread: long stretches share the taps and the window's first reads, short
-  // ones fill the machine. Steps and single channels keep 8 blocks for every SM. Prompts in
-  // vectors keep one: a prompt of 1024 tokens took 12 us at 8 per SM and 10 at 1, since every further
-  // block brings in its taps anew.
   const int64_t rows = step ? int64_t(a.R) * a.P : a.P;
   const int64_t seqs = step ? 1 : a.R;
-  a.tt = step ? 8 : 32;
-  const int least = step ? 2 : 4;
-  const int64_t least_blocks = int64_t(step || !wide ? 8 : 1) * sms;
   auto blocks = [&](int tt) {
     const int64_t n = (rows + int64_t(tt) * by - 1) / (int64_t(tt) * by);
     return (n < 1 ? 1 : n) * seqs * a.n_ctile;
   };
-  while (a.tt > least && blocks(a.tt) < least_blocks) a.tt /= 2;
+  // Tokens (beams) per thread: the count whose waves of blocks, two per SM, end first. A wave takes
+  // its count and a start (taps, window, the ring's first fill) worth 8 tokens, or a beam. Against
+  // powers of two that leave 1 (prompts) or 8 blocks for every SM: 1 x 1024 tokens of 6144 channels
+  // 8.3 us and 9.7, 4 x 1024 22 and 25, 8 x 5120 167 and 177, 1024 beams 18 and 26, 8192 beams 112
+  // both. Longer stretches: prompts up to 256 173 us (of 167), beams up to 16 114 (of 112).
+  const int64_t slots = 2 * int64_t(sms);
+  int64_t least = 0;
+  for (int tt = step ? 2 : 4; tt <= (step ? 12 : 64); tt += step ? 1 : 4) {
+    const int64_t cost = (blocks(tt) + slots - 1) / slots * (tt + (step ? 1 : 8));
+    if (!least || cost < least) {
+      least = cost;
+      a.tt = tt;
+    }
+  }
   const int64_t grid = blocks(a.tt);
   a.n_ttile = int(grid / seqs / a.n_ctile);
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
