@@ -72,7 +72,7 @@ struct Lay {
   static constexpr uint32_t kS = kXw + 3 * kBlk;           // state copy [64 KB rows][64 columns]
   static constexpr uint32_t kSc = kS + KB * 8192;          // scalars per stage
   static constexpr uint32_t kBar = kSc + NST * kScFloats * 4;
-  static constexpr int kNBar = 7 * NST + 12;
+  static constexpr int kNBar = 7 * NST + 13;
   static constexpr uint32_t kBad = kBar + kNBar * 8;       // flag
   // the tensor-memory address is handed over in the scalars' place, before they are written
   static constexpr uint32_t kBytes = kBad + 8;
@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   uint64_t* y_full = one + 9;            // Y1 and Y2 done
   uint64_t* y_free = one + 10;           // Y1 and Y2 read (NY warps)
   uint64_t* done = one + 11;             // every MMA completed (both issuers)
+  uint64_t* p_read = one + 12;           // P read by Y1 (commit)
   volatile uint32_t* bad = reinterpret_cast<uint32_t*>(sm + Y::kBad);   // a state is not finite
   uint32_t* holder = reinterpret_cast<uint32_t*>(sm + Y::kSc);
   const ScanArgs& a = c.a;
@@ -298,6 +299,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
     mbar_init(y_full, 1);
     mbar_init(y_free, NY);
     mbar_init(done, 2);
+    mbar_init(p_read, 1);
     *bad = 0;
     fence_barrier_init();
   }
@@ -369,13 +371,15 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
 #pragma unroll
               for (int k = 0; k < 8; ++k)
                 umma_bf16_ts(tmem + kTY1, tmem + kTG + k * 16, dv + k * 128, id_y, k != 0);
+              umma_commit(p_read);
             }
             __syncwarp();
           }
           if (i + 1 < nch) {
-            // G of the next chunk: queries x keys
+            // G of the next chunk: queries x keys. It takes P's place, and products of different
+            // shape and accumulator are not ordered by their issue: Y1 has to have read P
             const int s1 = (i + 1) % NST;
-            ok = warp_wait(&kq_full[s1], (i + 1) / NST);
+            ok = warp_wait(&kq_full[s1], (i + 1) / NST) && (i < 0 || warp_wait(p_read, i));
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {

@@ -1,0 +1,50 @@
+"""The operators around the recurrence at their edges: orderings that no result shows reliably, odd
+calls that the documentation allows, and values at the ends of their types."""
+import os
+import re
+
+import pytest
+import torch
+
+import layer_ref as ref
+import linear_attention_beam_gdn_b200 as ola
+from test_layer_ops import BF, F, L, _chunked, _scan_case, close, cu, same  # noqa: F401
+
+CSRC = os.path.join(ola.PKG_DIR, "csrc")
+
+
+# ----------------------------------------------------------------------------- chunked scan, order
+
+def test_chunk_scan_waits_before_it_overwrites_the_weights():
+    """Y1 reads the weights P from the tensor-memory columns that G of the next chunk is written to.
+    The two products differ in shape and accumulator, so nothing orders them but a completion
+    barrier: it has to be committed behind Y1 and waited for before G."""
+    with open(os.path.join(CSRC, "ola_scan_chunk.cu")) as f:
+        role = f.read().split("products Y1, G, Y2", 1)[1].split("// ----", 1)[0]
+    y1, g = role.index("umma_bf16_ts(tmem + kTY1"), role.index("umma_bf16(tmem + kTG")
+    assert y1 < g
+    commit = re.search(r"umma_commit\((\w+)\)", role[y1:g])
+    assert commit, "nothing tells when Y1 has read P"
+    assert f"warp_wait({commit.group(1)}, i)" in role[y1 + commit.end():g]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dk,H", [(128, 2), (64, 80)])
+def test_scan_long_prompt(dk, H):
+    """Thousands of tokens: in pieces of many chunks (few heads) and uncut; bit-equal from run to run."""
+    R, P, dv = 1, 6000, 64
+    c, o = _scan_case(BF, R, P, H, 1, dk, dv, D=True, state=True, seed=21)
+    cg = {n: t.cuda() for n, t in c.items()}
+    kw = dict(D=cu(o["D"]), dt_bias=cu(o["dt_bias"]), S_in=cu(o["S_in"]))
+    y, S = ola.scan(**cg, **kw)
+    assert ola.layer_status() == ola.OLA_OK
+    for _ in range(5):
+        y2, S2 = ola.scan(**cg, **kw)
+        same(y2, y, "y")
+        same(S2, S, "state")
+    h = slice(0, 2)                                      # every head alone is the same recurrence
+    y64, S64, ty, tS = ref.scan(c["v"][:, :, h], c["dt"][:, :, h], c["A"][h], c["k"], c["q"],
+                                o["D"][h], o["dt_bias"][h], None, o["S_in"][:, h], None, True,
+                                torch.zeros(R, P, 2, dv, dtype=BF), chunked=True)
+    close(y[:, :, h], y64, ty, "y")
+    close(S[:, h], S64, tS, "state")
