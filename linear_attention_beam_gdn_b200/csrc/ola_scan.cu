@@ -128,10 +128,10 @@ __global__ void __launch_bounds__(kScanThreads) scan_tok_kernel(ScanArgs a, int 
     if (tid < kTC) {
       float dt = raw + bias;
       if (a.softplus) dt = softplus_f(dt);
-      if (tid >= np) dt = 0.f;
       raw = load_dt(pt + kTC);
-      ds[b * kTC + tid] = dt;
-      as[b * kTC + tid] = expf(dt * A);
+      // rows behind the end add nothing and decay nothing (0 * A is NaN for an infinite A)
+      ds[b * kTC + tid] = tid < np ? dt : 0.f;
+      as[b * kTC + tid] = tid < np ? expf(dt * A) : 1.f;
     }
   };
   double logsum = 0.0;                             // sum of dt A over the piece
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_tok_kernel(ScanArgs a, int 
     }
   }
   if (!FULL && tid == 0 && blockIdx.y == 0)
-    a.seg_a[int64_t(rh) * a.nseg + seg] = float(exp(logsum * double(A)));
+    a.seg_a[int64_t(rh) * a.nseg + seg] = p0 < p1 ? float(exp(logsum * double(A))) : 1.f;
 }
 
 // The state before each piece from the pieces' own states: e_0 = S_in, e_(s+1) = a_s e_s + S_s.

@@ -494,14 +494,14 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
     float raw = c0 == 0 ? load_dt(0) : 0.f;
     auto scalars = [&](int i) -> bool {
       const int s = i % NST, n = i / NST;
-      // tokens behind the end take no part: dt = 0
+      // tokens behind the end take no part: dt = 0, no decay
       float dt = raw + bias;
       if (a.softplus) dt = softplus_f(dt);
       if (A2 != A2) dt = A2;                 // the clamp below would hide it
-      if (t >= p1 - (p0 + i * kQ)) dt = 0.f;
-      raw = load_dt(i + 1);
       // a decay below 2^-256 is 0; the clamp keeps sums of resets finite
       float sum = fmaxf(dt * A2, -256.f);
+      if (t >= p1 - (p0 + i * kQ)) dt = sum = 0.f;   // both: 0 * A is NaN for an infinite A
+      raw = load_dt(i + 1);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const float d = __shfl_down_sync(kFull, sum, o);

@@ -8,7 +8,7 @@ import torch
 
 import layer_ref as ref
 import linear_attention_beam_gdn_b200 as ola
-from test_layer_ops import BF, F, L, _chunked, _scan_case, close, cu, same  # noqa: F401
+from test_layer_ops import BF, F, _chunked, _scan_case, close, cu, same
 
 CSRC = os.path.join(ola.PKG_DIR, "csrc")
 
@@ -48,3 +48,28 @@ def test_scan_long_prompt(dk, H):
                                 torch.zeros(R, P, 2, dv, dtype=BF), chunked=True)
     close(y[:, :, h], y64, ty, "y")
     close(S[:, h], S64, tS, "state")
+
+
+# ----------------------------------------------------------------------------- values at the ends
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,P,H,lens", [(F, 130, 2, None), (F, 700, 1, [700, 333]),
+                                            (BF, 130, 2, None), (BF, 130, 80, [130, 65]),
+                                            (BF, 700, 1, [700, 333])])
+def test_scan_infinite_decay(dtype, P, H, lens):
+    """A = -inf forgets everything before each token; tokens behind a sequence's end (in the last
+    tile of a prompt, too) decay nothing. The definition with A = -1e6 is the same: exp(-1e4) = 0."""
+    R, dk, dv = 2, 64, 64
+    c, o = _scan_case(dtype, R, P, H, 1, dk, dv, bias=False, softplus=False, state=True, lens=lens,
+                      seed=31)
+    c["dt"] = c["dt"] + 0.05
+    c["A"][0] = -1e6
+    out0 = torch.full((R, P, H, dv), 3.0, dtype=dtype)
+    y64, S64, ty, tS = ref.scan(**c, D=None, dt_bias=None, z=None, S_in=o["S_in"], lens=o["lens"],
+                                use_softplus=False, out0=out0, chunked=_chunked(dtype, dk))
+    c["A"][0] = -float("inf")
+    y, S = ola.scan(**{n: t.cuda() for n, t in c.items()}, S_in=cu(o["S_in"]), softplus=False,
+                    lens=cu(o["lens"]), out=out0.cuda())
+    assert ola.layer_status() == ola.OLA_OK
+    close(y, y64, ty, "y")
+    close(S, S64, tS, "state")
