@@ -497,9 +497,11 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
       // tokens behind the end take no part: dt = 0, no decay
       float dt = raw + bias;
       if (a.softplus) dt = softplus_f(dt);
-      if (A2 != A2) dt = A2;                 // the clamp below would hide it
-      // a decay below 2^-256 is 0; the clamp keeps sums of resets finite
-      float sum = fmaxf(dt * A2, -256.f);
+      // a decay below 2^-256 is 0; the clamp keeps sums of resets finite. It would hide a decay that
+      // is not a number (A NaN, or 0 * inf): the token's weight becomes one then
+      const float e = dt * A2;
+      if (e != e) dt = e;
+      float sum = fmaxf(e, -256.f);
       if (t >= p1 - (p0 + i * kQ)) dt = sum = 0.f;   // both: 0 * A is NaN for an infinite A
       raw = load_dt(i + 1);
 #pragma unroll

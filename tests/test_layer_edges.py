@@ -73,3 +73,55 @@ def test_scan_infinite_decay(dtype, P, H, lens):
     assert ola.layer_status() == ola.OLA_OK
     close(y, y64, ty, "y")
     close(S, S64, tS, "state")
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,P,H,dk", [(BF, 200, 40, 128), (BF, 200, 40, 64), (BF, 1200, 2, 128),
+                                          (F, 300, 2, 64), (F, 800, 1, 32), (BF, 200, 2, 256)])
+@pytest.mark.parametrize("where", ["v", "k", "q", "dt", "z", "S_in", "decay"])
+def test_scan_non_finite_inputs(dtype, P, H, dk, where):
+    """A value that is not finite makes exactly those outputs and state elements not finite that the
+    formula makes so; all others are as good as ever."""
+    R, dv, G = 2, 64, 1
+    c, o = _scan_case(dtype, R, P, H, G, dk, dv, z=True, state=True, bias=False, softplus=False,
+                      lens=[P, P - 70], seed=41)
+    at = [(0, 10), (0, 140), (1, 127), (1, 63)]
+    for i, (r, p) in enumerate(at):
+        bad = (NAN, INF, -INF, NAN)[i]
+        h, e = i % H, (7 * i) % dv
+        if where in ("v", "z"):
+            (c if where == "v" else o)[where][r, p, h, e] = bad
+        elif where in ("k", "q"):
+            c[where][r, p, 0, (9 * i) % dk] = bad
+        elif where == "dt":
+            c["dt"][r, p, h] = abs(bad)
+        elif where == "S_in":
+            o["S_in"][r, h, e, (9 * i) % dk] = bad
+    if where == "decay":                                  # 0 * -inf: not a number from there on
+        c["A"][0] = -INF
+        c["dt"] = c["dt"] + 0.05
+        c["dt"][0, 140, 0] = c["dt"][1, 20, 0] = 0.0
+    out0 = torch.full((R, P, H, dv), 3.0, dtype=dtype)
+    want = dict(c)
+    if where == "decay":
+        # the bound is not made for an infinite A: this head is compared by where it is finite only
+        want["A"] = c["A"].clone()
+        want["A"][0] = -1e6
+    y64, S64, ty, tS = ref.scan(**want, D=None, dt_bias=None, z=o["z"], S_in=o["S_in"], lens=o["lens"],
+                                use_softplus=False, out0=out0, chunked=_chunked(dtype, dk))
+    if where == "decay":
+        y64[0, 140:, 0], S64[0, 0] = NAN, NAN
+        y64[1, 20:P - 70, 0], S64[1, 0] = NAN, NAN
+    y, S = ola.scan(**{n: t.cuda() for n, t in c.items()}, z=cu(o["z"]), S_in=cu(o["S_in"]),
+                    lens=cu(o["lens"]), softplus=False, out=out0.cuda())
+    assert ola.layer_status() == ola.OLA_OK
+    for got, w64, tol, what in ((y, y64, ty, "y"), (S, S64, tS, "state")):
+        got, fine = got.cpu().double(), torch.isfinite(w64)
+        assert torch.equal(torch.isfinite(got), fine), \
+            (what, (torch.isfinite(got) & ~fine).nonzero()[:4], (~torch.isfinite(got) & fine).nonzero()[:4])
+        zero = torch.zeros_like(w64)
+        close(torch.where(fine, got, zero), torch.where(fine, w64, zero),
+              torch.where(fine, tol, zero + 1), what)
