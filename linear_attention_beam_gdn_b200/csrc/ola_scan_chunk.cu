@@ -169,53 +169,121 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 }
 
 // A value that is not finite makes NaN of its products with the masked weights too, so of its
-// column's outputs earlier in its chunk. They are taken again, token by token from the piece's
-// start; a warp per column. From the value on the column's outputs and state are not finite anyway.
-__device__ __noinline__ void redo_column(const ScanArgs& a, const float* entering, int r, int h,
-                                         int g, int col, int p0, int p1) {
-  const int lane = threadIdx.x & 31;
-  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + int64_t(r) * a.v_seq +
-                           int64_t(h) * a.d_v + col;
-  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + int64_t(r) * a.k_seq +
-                           int64_t(g) * a.d_k;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + int64_t(r) * a.q_seq +
-                           int64_t(g) * a.d_k;
-  int first = p1;
-  for (int b = p0; b < p1 && first == p1; b += 32) {
-    const int p = b + lane;
-    const bool odd = p < p1 && !(fabsf(to_f32(v[int64_t(p) * a.v_tok])) < INFINITY);
-    const uint32_t m = __ballot_sync(kFull, odd);
-    if (m) first = b + __ffs(m) - 1;
+// column's outputs earlier in its chunk. They are taken again: the recurrence in fp32 from the
+// piece's start to the last such value, by the whole block over tiles staged in shared memory, where
+// a thread holds 8 key columns of one value column and warps without an affected column only stage.
+// From the value on the column's outputs and state are not finite anyway. Such values in one column at
+// token 5000 of 5120 (40 heads of 128 x 128) take a call of 125 us to 380 us, in 64 columns to 910
+// (two value columns per thread in half of the warps: 524 and 850; a warp per column that walks the
+// tokens in global memory: 7900 and 16400).
+__device__ __noinline__ void second_look(const ScanArgs& a, const float* entering,
+                                         unsigned char* sm, int r, int h, int g, int v0, int nv,
+                                         int p0, int p1) {
+  using bf16 = __nv_bfloat16;
+  constexpr int kRow = 128;                        // key columns of a staged row, filled up
+  bf16* ks = reinterpret_cast<bf16*>(sm);          // [kQ][kRow], then the same of q
+  bf16* qs = ks + kQ * kRow;
+  bf16* vs = qs + kQ * kRow;                       // [kQ][kNV]
+  float2* al = reinterpret_cast<float2*>(vs + kQ * kNV);   // [kQ] decay, dt
+  int* first = reinterpret_cast<int*>(al + kQ);    // [kNV] a column's first bad token
+  int* last = first + kNV;                         // behind the last output to be taken
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bf16* v = static_cast<const bf16*>(a.v) + int64_t(r) * a.v_seq + int64_t(h) * a.d_v + v0;
+  const bf16* k = static_cast<const bf16*>(a.k) + int64_t(r) * a.k_seq + int64_t(g) * a.d_k;
+  const bf16* q = static_cast<const bf16*>(a.q) + int64_t(r) * a.q_seq + int64_t(g) * a.d_k;
+  __syncthreads();                                 // every role is done with shared memory
+  if (tid < kNV) first[tid] = p1;
+  if (tid == kNV) *last = p0;
+  __syncthreads();
+  if (2 * lane < nv) {
+#pragma unroll 4
+    for (int p = p0 + warp; p < p1; p += kThr / 32) {
+      const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(v + int64_t(p) * a.v_tok) + lane);
+      if ((x & 0x7f80u) == 0x7f80u) atomicMin(first + 2 * lane, p);
+      if ((x & 0x7f800000u) == 0x7f800000u) atomicMin(first + 2 * lane + 1, p);
+    }
   }
-  if (first == p1) return;
-  const int chunk = p0 + (first - p0) / kQ * kQ;
-  float S[4];
+  __syncthreads();
+  // this thread's value column, its outputs [from, to) and 8 key columns
+  const int c = tid >> 4, kg = tid & 15;
+  const int to = c < nv ? first[c] : p1, from = p0 + (to - p0) / kQ * kQ;
+  const bool mine = to < p1 && from < to;
+  if (mine && kg == 0) atomicMax(last, to);
+  __syncthreads();
+  const int end = *last;
+  uint64_t S[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int e = lane + 32 * j;
-    S[j] = entering && e < a.d_k ? entering[int64_t(col) * a.d_k + e] : 0.f;
+    const int e = 8 * kg + 2 * j;
+    const float* s = entering + int64_t(v0 + c) * a.d_k + e;
+    S[j] = entering && mine && e < a.d_k ? f2(s[0], s[1]) : f2(0.f, 0.f);
   }
-  for (int p = p0; p < first; ++p) {
-    float dt = a.dt[(int64_t(r) * a.P + p) * a.H + h] + (a.dt_bias ? a.dt_bias[h] : 0.f);
-    if (a.softplus) dt = softplus_f(dt);
-    const float al = expf(dt * a.A[h]), vp = to_f32(v[int64_t(p) * a.v_tok]), w = dt * vp;
-    float o = 0.f;
+  const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, D = a.D ? a.D[h] : 0.f;
+  auto pairs = [](const bf16* p, uint64_t (&x)[4]) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    x[0] = u2(w.x << 16, w.x & 0xffff0000u);
+    x[1] = u2(w.y << 16, w.y & 0xffff0000u);
+    x[2] = u2(w.z << 16, w.z & 0xffff0000u);
+    x[3] = u2(w.w << 16, w.w & 0xffff0000u);
+  };
+  auto step = [&](int t) {
+    const float2 ad = al[t];
+    const float w1 = ad.y * to_f32(vs[t * kNV + c]);
+    const uint64_t w = f2(w1, w1), d = f2(ad.x, ad.x);
+    uint64_t kk[4];
+    pairs(ks + t * kRow + 8 * kg, kk);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int e = lane + 32 * j;
-      if (e >= a.d_k) break;
-      S[j] = fmaf(al, S[j], w * to_f32(k[int64_t(p) * a.k_tok + e]));
-      if (p >= chunk) o = fmaf(S[j], to_f32(q[int64_t(p) * a.q_tok + e]), o);
+    for (int j = 0; j < 4; ++j) S[j] = fma2(d, S[j], mul2(w, kk[j]));
+  };
+  for (int pt = p0; pt < end; pt += kQ) {
+    const int n = min(kQ, end - pt);
+    const bool here = mine && from == pt;
+    const bool outputs = __syncthreads_or(here);   // and: the tile before was read
+    const uint4 z4 = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < n * (kRow / 8); i += kThr) {
+      const int t = i / (kRow / 8), e = i % (kRow / 8) * 8;
+      const bool in = e < a.d_k;
+      const int64_t p = pt + t;
+      *reinterpret_cast<uint4*>(ks + t * kRow + e) =
+          in ? __ldg(reinterpret_cast<const uint4*>(k + p * a.k_tok + e)) : z4;
+      if (outputs)
+        *reinterpret_cast<uint4*>(qs + t * kRow + e) =
+            in ? __ldg(reinterpret_cast<const uint4*>(q + p * a.q_tok + e)) : z4;
     }
-    if (p < chunk) continue;
-    o = group_sum(o, 32);
-    if (a.D) o = fmaf(a.D[h], vp, o);
-    if (a.z)
-      o *= silu_f<__nv_bfloat16>(to_f32(static_cast<const __nv_bfloat16*>(
-          a.z)[int64_t(r) * a.z_seq + int64_t(p) * a.z_tok + int64_t(h) * a.d_v + col]));
-    if (lane == 0)
-      static_cast<__nv_bfloat16*>(a.y)[int64_t(r) * a.y_seq + int64_t(p) * a.y_tok +
-                                       int64_t(h) * a.d_v + col] = from_f32<__nv_bfloat16>(o);
+    for (int i = tid; i < n * (kNV / 8); i += kThr) {
+      const int t = i / (kNV / 8), e = i % (kNV / 8) * 8;
+      *reinterpret_cast<uint4*>(vs + t * kNV + e) =
+          e < nv ? __ldg(reinterpret_cast<const uint4*>(v + int64_t(pt + t) * a.v_tok + e)) : z4;
+    }
+    if (tid < n) {
+      float dt = __ldg(a.dt + (int64_t(r) * a.P + pt + tid) * a.H + h) + bias;
+      if (a.softplus) dt = softplus_f(dt);
+      al[tid] = make_float2(expf(dt * A), dt);
+    }
+    __syncthreads();
+    if (!__any_sync(kFull, mine && pt < to)) continue;
+    if (!__any_sync(kFull, here)) {
+#pragma unroll 4
+      for (int t = 0; t < n; ++t) step(t);
+      continue;
+    }
+    for (int t = 0; t < n; ++t) {
+      step(t);
+      uint64_t qq[4], acc = f2(0.f, 0.f);
+      pairs(qs + t * kRow + 8 * kg, qq);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc = fma2(S[j], qq[j], acc);
+      const float2 h2 = un2(acc);
+      float o = group_sum(h2.x + h2.y, 16);
+      const int64_t p = pt + t;
+      if (!here || kg != 0 || p >= to) continue;
+      if (a.D) o = fmaf(D, to_f32(vs[t * kNV + c]), o);
+      const int64_t col = int64_t(h) * a.d_v + v0 + c;
+      if (a.z)
+        o *= silu_f<bf16>(to_f32(
+            static_cast<const bf16*>(a.z)[int64_t(r) * a.z_seq + p * a.z_tok + col]));
+      static_cast<bf16*>(a.y)[int64_t(r) * a.y_seq + p * a.y_tok + col] = from_f32<bf16>(o);
+    }
   }
 }
 
@@ -855,8 +923,7 @@ __global__ void __launch_bounds__(kThr, 1) scan_chunk_kernel(const __grid_consta
   tc_fence_after();
   if (FULL && *bad) {
     // every output has been stored by now
-    for (int col = warp; col < nv; col += kThr / 32)
-      redo_column(a, entering, r, h, g, v0 + col, p0, p1);
+    second_look(a, entering, sm, r, h, g, v0, nv, p0, p1);
     __syncthreads();
   }
   if (late && out && warp >= 24 && warp < 28) {

@@ -125,3 +125,42 @@ def test_scan_non_finite_inputs(dtype, P, H, dk, where):
         zero = torch.zeros_like(w64)
         close(torch.where(fine, got, zero), torch.where(fine, w64, zero),
               torch.where(fine, tol, zero + 1), what)
+
+
+def _time(fn, n=5):
+    fn()
+    ts = []
+    for _ in range(n):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        fn()
+        b.record()
+        b.synchronize()
+        ts.append(a.elapsed_time(b))
+    return min(ts)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cols", [1, 64])
+def test_scan_late_bad_value_costs_a_second_look_not_a_walk(cols):
+    """The outputs before a value that is not finite, in its own chunk, are taken again from the
+    state before the chunk. That is work of the order of the call itself."""
+    R, P, H, dk, dv = 1, 5120, 40, 128, 128
+    c, _ = _scan_case(BF, R, P, H, 1, dk, dv, bias=False, seed=51)
+    cg = {n: t.cuda() for n, t in c.items()}
+    out, S = torch.empty_like(cg["v"]), torch.empty(R, H, dv, dk, device="cuda")
+    clean = _time(lambda: ola.scan(**cg, out=out, S_out=S))
+    y0 = out.clone()
+    p = 5000
+    cg["v"][0, p, 3, :cols] = NAN
+    dirty = _time(lambda: ola.scan(**cg, out=out, S_out=S))
+    assert not torch.isfinite(out[0, p:, 3, :cols]).any()
+    h = slice(3, 4)
+    y64, _, ty, _ = ref.scan(c["v"][:, :p, h], c["dt"][:, :p, h], c["A"][h], c["k"][:, :p],
+                             c["q"][:, :p], None, None, None, None, None, True,
+                             torch.zeros(R, p, 1, dv, dtype=BF), chunked=True)
+    close(out[:, :p, h], y64, ty, "y before it")
+    y0[0, :, 3, :cols] = out[0, :, 3, :cols] = 0.0
+    same(out, y0, "y elsewhere")
+    print(f"clean {clean * 1e3:.0f} us, one bad token in {cols} columns {dirty * 1e3:.0f} us")
+    assert dirty <= 16 * clean, (clean, dirty)
