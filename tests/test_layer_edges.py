@@ -2,13 +2,14 @@
 calls that the documentation allows, and values at the ends of their types."""
 import os
 import re
+import subprocess
 
 import pytest
 import torch
 
 import layer_ref as ref
 import linear_attention_beam_gdn_b200 as ola
-from test_layer_ops import BF, F, _chunked, _scan_case, close, cu, same
+from test_layer_ops import BF, F, _chunked, _scan_case, close, cu, gen, same
 
 CSRC = os.path.join(ola.PKG_DIR, "csrc")
 
@@ -164,3 +165,104 @@ def test_scan_late_bad_value_costs_a_second_look_not_a_walk(cols):
     same(out, y0, "y elsewhere")
     print(f"clean {clean * 1e3:.0f} us, one bad token in {cols} columns {dirty * 1e3:.0f} us")
     assert dirty <= 16 * clean, (clean, dirty)
+
+
+# ----------------------------------------------------------------------------- calls of every kind
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R", [1, 3])
+def test_one_token_slices_of_one_buffer(R):
+    """One token of each of R requests: inputs and outputs are column slices of one buffer."""
+    H, d, W = 2, 32, 4
+    C = H * d
+    buf = gen(R, 1, 7 * C, dtype=BF, seed=61).cuda()
+    part = lambda i: buf[:, :, i * C:(i + 1) * C]  # noqa: E731
+    heads = lambda i: part(i).unflatten(2, (H, d))  # noqa: E731
+    w, win = gen(C, W, seed=62).cuda(), gen(R, 1, W - 1, C, dtype=BF, seed=63).cuda()
+    y0, s0 = ola.conv_step(part(0).contiguous(), w, state=win)
+    y1, s1 = ola.conv_step(part(0), w, state=win, out=part(4))
+    same(part(4).contiguous(), y0, "convolution step")
+    same(s1, s0, "window")
+    ola.conv(part(0), w, state=win[:, 0].contiguous(), out=part(5))
+    same(part(5).contiguous(), y0, "convolution")
+    dt, A = gen(R, 1, H, seed=64).cuda(), -torch.ones(H).cuda()
+    S = gen(R, 1, H, d, d, seed=65).cuda()
+    args = [heads(i).contiguous() for i in (1, 2, 3)]
+    y0, S0 = ola.scan_step(args[0], dt, A, args[1], args[2], state=S)
+    _, S1 = ola.scan_step(heads(1), dt, A, heads(2), heads(3), state=S, out=heads(6))
+    same(heads(6).contiguous(), y0, "scan step")
+    same(S1, S0, "state")
+    y0, S0 = ola.scan(args[0], dt, A, args[1], args[2], S_in=S[:, 0].contiguous())
+    ola.scan(heads(1), dt, A, heads(2), heads(3), S_in=S[:, 0].contiguous(), out=heads(4))
+    same(heads(4).contiguous(), y0, "scan")
+    for i in (1, 2, 3):                                   # a real overlap is still refused
+        with pytest.raises(ola.OlaError):
+            ola.scan_step(heads(1), dt, A, heads(2), heads(3), state=S, out=heads(i))
+
+
+# ----------------------------------------------------------------------------- strides and overlaps
+
+DRIVER = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+
+#include "ola_rows.h"
+
+int main(int n, char** v) {
+  int64_t x[16] = {};
+  for (int i = 2; i < n && i < 18; ++i) x[i - 2] = strtoll(v[i], nullptr, 0);
+  auto rows = [&](int i) {
+    return ola::Rows{reinterpret_cast<const void*>(x[i]), x[i + 1], x[i + 2], x[i + 3], x[i + 4],
+                     x[i + 5], int(x[i + 6])};
+  };
+  if (!strcmp(v[1], "overlap")) {
+    ola::Rows a = rows(0), b = rows(7);
+    if (!ola::strides(&a, false) || !ola::strides(&b, true)) return 2;
+    printf("%d", ola::overlap(a, b));
+  } else if (!strcmp(v[1], "strides")) {
+    ola::Rows a = rows(0);
+    printf("%d", ola::strides(&a, x[7]));
+  }
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def rows(tmp_path_factory):
+    """The library's checks of row tensors, compiled so that a signed overflow ends the process."""
+    d = tmp_path_factory.mktemp("rows")
+    (d / "rows.cpp").write_text(DRIVER)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=signed-integer-overflow",
+                    "-fsanitize-undefined-trap-on-error", "-I", CSRC, "-o", str(d / "rows"),
+                    str(d / "rows.cpp")], check=True)
+
+    def call(what, *args):
+        p = subprocess.run([str(d / "rows"), what, *map(str, args)], capture_output=True, text=True)
+        assert p.returncode == 0, (what, args, p.returncode)
+        return int(p.stdout)
+
+    return call
+
+
+@pytest.mark.parametrize("R,P", [(1, 1), (3, 1), (1, 4), (3, 4)])
+def test_overlap_of_column_slices(rows, R, P):
+    """Column slices of one [R, P, wide] buffer share bytes where their columns do, also with one
+    token per sequence, where the token stride is not used."""
+    wide, e, base = 700, 2, 1 << 20
+
+    def at(col, width):
+        tok = wide if P > 1 else 0                        # as the Python binding passes them
+        return (base + col * e, R, P, tok, P * wide, width, e)
+
+    # column, width of an input; of the output
+    for i, o, want in (((0, 100), (100, 100), 0), ((100, 100), (0, 100), 0), ((0, 100), (600, 100), 0),
+                       ((0, 64), (100, 100), 0), ((500, 100), (100, 400), 0), ((0, 100), (99, 100), 1),
+                       ((100, 100), (0, 101), 1), ((0, 700), (300, 10), 1), ((300, 10), (0, 700), 1),
+                       ((0, 100), (0, 100), 1)):
+        assert rows("overlap", *at(*i), *at(*o)) == want, (i, o)
+    # another buffer behind the first, and one that starts inside it
+    behind = (base + R * P * wide * e, R, P, 0, 0, 100, e)
+    inside = (base + 50 * e, 1, 1, 0, 0, 100, e)
+    assert rows("overlap", *at(0, 100), *behind) == 0
+    assert rows("overlap", *at(0, 100), *inside) == 1
