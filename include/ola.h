@@ -266,6 +266,7 @@ ola_status ola_decode_noalloc(const ola_geometry* geom, const float* S_ctx, cons
  * - Strides are in elements, "tok" between consecutive tokens (or beams) and "seq" between
  *   sequences; 0 stands for the contiguous value. Channels (heads x width) are contiguous.
  *   A tok stride is at least the row's width; a sequence may not overlap the next one in outputs.
+ *   No tensor may span more than 2^46 elements.
  * - lens: device [R] int32 or NULL: sequence r has min(max(lens[r], 0), P) tokens and the rows
  *   behind them are padding, never read into a result; the output rows there keep what they held.
  * - parent_idx: device [R][B] int32 or NULL: beam b continues state parent_idx[r][b] of the Bp

@@ -199,7 +199,8 @@ ola_status ola_conv(const ola_conv_desc* d, const void* x, const float* w, const
   Rows rx, ry;
   ola_status s = conv_args(d, x, w, bias, y, &a, &rx, &ry);
   if (s != OLA_OK) return s;
-  const int64_t n = int64_t(d->R) * (d->W - 1) * d->C;
+  int64_t n;
+  if (!elements({d->R, d->W - 1, d->C}, &n)) return OLA_ERR_UNSUPPORTED;
   const Rows si = flat(state_in, n, rx.e), so = flat(state_out, n, rx.e);
   if (!aligned(state_in, rx.e) || !aligned(state_out, rx.e) || !aligned(lens, 4))
     return OLA_ERR_INVALID_ARG;
@@ -225,9 +226,10 @@ ola_status ola_conv_step(const ola_conv_desc* d, int32_t Bp, const void* x, cons
   if (s != OLA_OK) return s;
   if (d->P < 1 || Bp < 1 || !state_in || !state_out) return OLA_ERR_INVALID_ARG;
   if (!parent_idx && Bp != 1 && Bp != d->P) return OLA_ERR_INVALID_ARG;
-  const int64_t one = int64_t(d->W - 1) * d->C;
-  const Rows si = flat(state_in, int64_t(d->R) * Bp * one, rx.e);
-  const Rows so = flat(state_out, int64_t(d->R) * d->P * one, rx.e);
+  int64_t ni, no;
+  if (!elements({d->R, Bp, d->W - 1, d->C}, &ni) || !elements({d->R, d->P, d->W - 1, d->C}, &no))
+    return OLA_ERR_UNSUPPORTED;
+  const Rows si = flat(state_in, ni, rx.e), so = flat(state_out, no, rx.e);
   if (!aligned(state_in, rx.e) || !aligned(state_out, rx.e) || !aligned(parent_idx, 4))
     return OLA_ERR_INVALID_ARG;
   if (overlap(rx, so) || overlap(ry, si) || overlap(ry, so)) return OLA_ERR_INVALID_ARG;
@@ -370,9 +372,11 @@ ola_status ola_scan_step(const ola_scan_desc* d, int32_t Bp, const void* v, cons
   if (!parent_idx && Bp != 1 && Bp != d->P) return OLA_ERR_INVALID_ARG;
   if (!aligned(state_in, 16) || !aligned(state_out, 16) || !aligned(parent_idx, 4))
     return OLA_ERR_INVALID_ARG;
-  const int64_t one = int64_t(d->H) * d->d_v * d->d_k;
-  const Rows si = flat(state_in, int64_t(d->R) * Bp * one, 4);
-  const Rows so = flat(state_out, int64_t(d->R) * d->P * one, 4);
+  int64_t ni, no;
+  if (!elements({d->R, Bp, d->H, d->d_v, d->d_k}, &ni) ||
+      !elements({d->R, d->P, d->H, d->d_v, d->d_k}, &no))
+    return OLA_ERR_UNSUPPORTED;
+  const Rows si = flat(state_in, ni, 4), so = flat(state_out, no, 4);
   const bool in_place = state_in == state_out && !parent_idx && Bp == d->P;
   if (!in_place && overlap(si, so)) return OLA_ERR_INVALID_ARG;
   for (const Rows* x : {&t.v, &t.k, &t.q, &t.z, &t.y})

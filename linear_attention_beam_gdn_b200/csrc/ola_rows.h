@@ -16,15 +16,32 @@ struct Rows {
   int64_t extent() const { return ((R - 1) * seq + (P - 1) * tok + width) * e; }
 };
 
-// Fills in default strides; false if they cannot be what the rows need.
+constexpr int64_t kMostElements = int64_t(1) << 46;   // byte offsets stay far inside 64 bits
+
+// Fills in default strides; false if they cannot be what the rows need. Every bound is tested before
+// the product that it bounds.
 inline bool strides(Rows* t, bool output) {
+  const int64_t most = kMostElements;
   if (t->tok == 0) t->tok = t->width;
+  if (t->tok < t->width || t->tok >= most || (t->P > 1 && t->tok > most / t->P)) return false;
   if (t->seq == 0) t->seq = t->P * t->tok;
-  if (t->tok < t->width || t->seq < 0) return false;
-  if (output && t->R > 1 && t->P > 0 && t->seq < (t->P - 1) * t->tok + t->width) return false;
-  const int64_t most = int64_t(1) << 46;          // byte offsets stay far inside 64 bits
-  return t->tok < most && t->seq < most && (t->R < 2 || t->seq <= most / t->R) &&
-         (t->P < 2 || t->tok <= most / t->P);
+  if (t->seq < 0 || t->seq >= most || (t->R > 1 && t->seq > most / t->R)) return false;
+  return !(output && t->R > 1 && t->P > 0 && t->seq < (t->P - 1) * t->tok + t->width);
+}
+
+// Product of sizes; false if it is above kMostElements.
+inline bool elements(std::initializer_list<int64_t> sizes, int64_t* n) {
+  *n = 1;
+  for (int64_t s : sizes)
+    if (s == 0) {
+      *n = 0;
+      return true;
+    }
+  for (int64_t s : sizes) {
+    if (s < 0 || *n > kMostElements / s) return false;
+    *n *= s;
+  }
+  return true;
 }
 
 // Whether two row sets share bytes. Column slices of one wide buffer (equal token strides, sequence

@@ -1,5 +1,6 @@
 """The operators around the recurrence at their edges: orderings that no result shows reliably, odd
 calls that the documentation allows, and values at the ends of their types."""
+import ctypes
 import os
 import re
 import subprocess
@@ -266,3 +267,23 @@ def test_overlap_of_column_slices(rows, R, P):
     inside = (base + 50 * e, 1, 1, 0, 0, 100, e)
     assert rows("overlap", *at(0, 100), *behind) == 0
     assert rows("overlap", *at(0, 100), *inside) == 1
+
+
+@pytest.mark.parametrize("R,P,tok,seq,output", [
+    (2, 5, 1 << 62, 0, 0), (2, 5, 1 << 62, 0, 1), (2, 5, 1 << 62, 100, 1), (2, 3, 1 << 45, 0, 1),
+    (1 << 30, 2, 0, 1 << 40, 1), (1, 1 << 30, 1 << 40, 0, 0), (2, 1, 0, (1 << 63) - 1, 1)])
+def test_strides_too_large_are_refused_without_overflow(rows, R, P, tok, seq, output):
+    assert rows("strides", 1 << 20, R, P, tok, seq, 16, 4, output) == 0
+
+
+def test_refuses_more_elements_than_64_bits_hold():
+    """Products of sizes past 2^46, the state counts of a step among them, are refused, not wrapped."""
+    L, far = ola.lib(), [(i + 1) << 52 for i in range(12)]
+    top = (1 << 31) - 1
+    c = ola.ConvDesc(top, 0, top, 4, ola.OLA_F32, 1, 0, 0, 0, 0)
+    assert L.ola_conv(ctypes.byref(c), *far[:7], None) == ola.OLA_ERR_UNSUPPORTED
+    c = ola.ConvDesc(1 << 16, 1, 1 << 16, 4, ola.OLA_F32, 1, 0, 0, 0, 0)
+    assert L.ola_conv_step(ctypes.byref(c), top, *far[:4], far[4], *far[5:7], None) == \
+        ola.OLA_ERR_UNSUPPORTED
+    d = ola.ScanDesc(1 << 12, 1, 1 << 12, 1, 256, 256, ola.OLA_F32, 1, *[0] * 10)
+    assert L.ola_scan_step(ctypes.byref(d), top, *far, None) == ola.OLA_ERR_UNSUPPORTED
