@@ -279,8 +279,9 @@ ola_status ola_decode_noalloc(const ola_geometry* geom, const float* S_ctx, cons
  * - Forward only, like every operator of the library: nothing is kept for gradients. */
 
 /* Wait for `stream`, return the first device-side error that a call of this section recorded on
- * the current device since the last ola_layer_status (OLA_OK if none), and clear it. Not to be
- * called while `stream` is being captured. Errors: CUDA. */
+ * the current device since the last ola_layer_status (OLA_OK if none), and clear it. There is one
+ * word for all streams and threads: reading and clearing are one step, and an error goes to one of
+ * several callers. Not to be called while `stream` is being captured. Errors: CUDA. */
 ola_status ola_layer_status(void* stream);
 
 /* Short depthwise causal convolution of W taps over u = state ++ x (the W-1 tokens before the

@@ -1,5 +1,6 @@
 // Host side of the operators around the recurrence declared in include/ola.h: argument checks,
 // dispatch, and the per-device error word that their kernels report to.
+#include <atomic>
 #include <initializer_list>
 #include <mutex>
 
@@ -10,6 +11,9 @@ using namespace ola;
 
 // code, detail, index of the first error recorded since it was last read (see report_error)
 static __device__ int g_layer_err[4];
+// what status calls took from it, a slot for each call under way
+constexpr int kTaken = 1024;
+static __device__ int g_layer_taken[kTaken];
 
 namespace {
 
@@ -24,6 +28,9 @@ ola_status from_cuda(cudaError_t e) {
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 bool width_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128 || d == 256; }
+
+// Reads and clears the error code in one step, so that each recorded error goes to one caller.
+__global__ void take_error_kernel(int slot) { g_layer_taken[slot] = atomicExch(g_layer_err, 0); }
 
 // Device address of the error word, resolved once per device; refuses devices the library was
 // not built for.
@@ -180,16 +187,18 @@ ola_status ola_layer_status(void* stream) {
   int* err = nullptr;
   ola_status s = error_word(&err);
   if (s != OLA_OK) return s;
+  static std::atomic<unsigned> calls{0};
+  const int slot = int(calls.fetch_add(1, std::memory_order_relaxed) % kTaken);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int word[4] = {0, 0, 0, 0};
-  cudaError_t e = cudaMemcpyAsync(word, err, sizeof(word), cudaMemcpyDeviceToHost, st);
+  int code = 0;
+  take_error_kernel<<<1, 1, 0, st>>>(slot);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess)
+    e = cudaMemcpyFromSymbolAsync(&code, g_layer_taken, sizeof(int), slot * sizeof(int),
+                                  cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  if (e == cudaSuccess && word[0] != 0) {
-    e = cudaMemsetAsync(err, 0, sizeof(word), st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  }
   if (e != cudaSuccess) return from_cuda(e);
-  return static_cast<ola_status>(word[0]);
+  return static_cast<ola_status>(code);
 }
 
 ola_status ola_conv(const ola_conv_desc* d, const void* x, const float* w, const float* bias,

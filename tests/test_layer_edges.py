@@ -4,6 +4,7 @@ import ctypes
 import os
 import re
 import subprocess
+import threading
 
 import pytest
 import torch
@@ -199,6 +200,39 @@ def test_one_token_slices_of_one_buffer(R):
     for i in (1, 2, 3):                                   # a real overlap is still refused
         with pytest.raises(ola.OlaError):
             ola.scan_step(heads(1), dt, A, heads(2), heads(3), state=S, out=heads(i))
+
+
+@pytest.mark.gpu
+def test_status_reports_every_error_once():
+    """Threads that read the error word on streams of their own: each recorded error is returned to
+    exactly one of them."""
+    # one beam of 8 bf16 channels: one device thread reads the parent, so a call records one error
+    x, w, st = gen(1, 1, 8, dtype=BF).cuda(), gen(8, 4, seed=1).cuda(), \
+        gen(1, 1, 3, 8, dtype=BF, seed=3).cuda()
+    bad = torch.tensor([[4]], dtype=torch.int32).cuda()
+    assert ola.layer_status() == ola.OLA_OK
+    torch.cuda.synchronize()
+    L, n, stop, seen = ola.lib(), 1000, threading.Event(), [0, 0, 0]
+
+    def poll(i):
+        side = torch.cuda.Stream()
+        while not stop.is_set():
+            for _ in range(50):
+                seen[i] += L.ola_layer_status(side.cuda_stream) == ola.OLA_ERR_BAD_PARENT
+
+    threads = [threading.Thread(target=poll, args=(i,)) for i in (1, 2)]
+    for t in threads:
+        t.start()
+    here = torch.cuda.current_stream().cuda_stream
+    try:
+        for _ in range(n):
+            ola.conv_step(x, w, state=st, parent_idx=bad)
+            seen[0] += L.ola_layer_status(here) == ola.OLA_ERR_BAD_PARENT
+    finally:
+        stop.set()
+        for t in threads:
+            t.join()
+    assert sum(seen) == n and ola.layer_status() == ola.OLA_OK, seen
 
 
 # ----------------------------------------------------------------------------- strides and overlaps
