@@ -446,7 +446,7 @@ class Decoder:
 
 # ------------------------------------------------------------------ operators around the recurrence
 #
-# Each call runs on the device of its first tensor and on `stream` (default: that device's current
+# Each call runs on the device of its first tensor and on `stream` of it (default: its current
 # stream), allocates only the outputs and scratch that it is not given (they belong to that
 # stream), and does not wait. Inputs that may be strided are [sequence, token, ...] with contiguous
 # channels, so a slice of a wide projection's columns is taken as it is. A decode step of a few
@@ -491,8 +491,12 @@ class _Here:
 
 def _scope(index, stream):
     c = _torch()._C
-    if stream is None and c._cuda_getDevice() == index:
-        return _Here(c._cuda_getCurrentRawStream(index))
+    if stream is None:
+        if c._cuda_getDevice() == index:
+            return _Here(c._cuda_getCurrentRawStream(index))
+    elif stream.device_index != index:
+        # the kernels would run on that device with another one's pointers
+        raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
     return _Scope(index, stream)
 
 
@@ -568,8 +572,15 @@ def _opt_rows(x, name, shape, dtype, index):
 
 def layer_status(device=None, stream=None) -> int:
     """Waits for `stream` and returns the first device-side error that an operator recorded on
-    `device` (default: the current one) since the last call (OLA_OK if none), and clears it."""
+    `device` (default: the stream's, or the current one) since the last call (OLA_OK if none), and
+    clears it."""
     torch = _torch()
+    if stream is not None:
+        index = torch.device(device).index if isinstance(device, str) else \
+            getattr(device, "index", device)
+        if index is not None and index != stream.device_index:
+            raise ValueError(f"stream is on cuda:{stream.device_index}, not on {device}")
+        device = stream.device_index
     with torch.cuda.device(device):
         st = ola_layer_status(_stream_ptr(stream))
     if st in (OLA_ERR_CUDA, OLA_ERR_UNSUPPORTED):

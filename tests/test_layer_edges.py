@@ -235,6 +235,20 @@ def test_status_reports_every_error_once():
     assert sum(seen) == n and ola.layer_status() == ola.OLA_OK, seen
 
 
+def test_refuses_a_stream_of_another_device():
+    """Kernels would run on the stream's device with pointers of another one."""
+    class Stream:
+        device_index = 1
+        device = torch.device("cuda", 1)
+        cuda_stream = 0
+
+    with pytest.raises(ValueError, match="stream"):
+        ola._scope(0, Stream())
+    for device in (0, "cuda:0", torch.device("cuda", 0)):
+        with pytest.raises(ValueError, match="stream"):
+            ola.layer_status(device, Stream())
+
+
 # ----------------------------------------------------------------------------- strides and overlaps
 
 DRIVER = r"""
