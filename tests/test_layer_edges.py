@@ -11,7 +11,7 @@ import torch
 
 import layer_ref as ref
 import linear_attention_beam_gdn_b200 as ola
-from test_layer_ops import BF, F, _chunked, _scan_case, close, cu, gen, same
+from test_layer_ops import BF, F, SCAN, _chunked, _scan_case, close, cu, gen, same
 
 CSRC = os.path.join(ola.PKG_DIR, "csrc")
 
@@ -54,6 +54,30 @@ def test_scan_long_prompt(dk, H):
 
 
 # ----------------------------------------------------------------------------- values at the ends
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F, BF])
+def test_silu_of_large_negative_values(dtype):
+    """u / (1 + e^-u) goes to 0 below, however large u is; -inf and NaN give NaN, +inf itself."""
+    u = torch.tensor([-3e38, -1e38, -1e30, -1e20, -1e6, -1000.0, -105.0, -104.0, -103.0, -89.0, -88.5,
+                      -88.0, -87.0, -50.0, -1.0, 0.0, 1.0, 88.0, 1e30, 3e38, -float("inf"),
+                      float("inf"), float("nan")]).to(dtype)
+    x = u[None, None]
+    w = torch.zeros(u.numel(), 2)
+    w[:, 1] = 1.0
+    y, _ = ola.conv(x.cuda(), w.cuda())
+    u64 = u.double()
+    want = u64 / (1 + torch.exp(-u64))
+    y = y.cpu().double()[0, 0]
+    assert torch.equal(torch.isnan(y), torch.isnan(want)), y
+    inf = torch.isinf(want)
+    assert torch.equal(y[inf], want[inf])
+    # the steps of the division and the result's rounding; below -87, where fp32's exponent ends,
+    # the result may be 0 or up to 104 e^-88 (6.3e-37)
+    rel = 8 * 2.0 ** -24 if dtype == F else 2.0 ** -8 + 2.0 ** -20
+    fine = ~torch.isnan(want) & ~inf
+    assert bool(((y - want).abs()[fine] <= rel * want.abs()[fine] + 1.5e-36).all()), (y, want)
+
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype,P,H,lens", [(F, 130, 2, None), (F, 700, 1, [700, 333]),
@@ -335,3 +359,51 @@ def test_refuses_more_elements_than_64_bits_hold():
         ola.OLA_ERR_UNSUPPORTED
     d = ola.ScanDesc(1 << 12, 1, 1 << 12, 1, 256, 256, ola.OLA_F32, 1, *[0] * 10)
     assert L.ola_scan_step(ctypes.byref(d), top, *far, None) == ola.OLA_ERR_UNSUPPORTED
+
+
+# ----------------------------------------------------------------------------- alignments
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,C,off,wide", [(BF, 64, 4, 72), (BF, 66, 2, 132), (BF, 1000, 4, 1004),
+                                              (BF, 6, 2, 10), (F, 18, 2, 22), (F, 64, 2, 66)])
+@pytest.mark.parametrize("W", [2, 4])
+def test_conv_rows_aligned_to_8_and_4_bytes(dtype, C, off, wide, W):
+    R, P = 3, 61
+    big = gen(R, P, wide, dtype=dtype, seed=71)
+    w, b = gen(C, W, seed=72), gen(C, seed=73)
+    st = gen(R, W - 1, C, dtype=dtype, seed=74)
+    lens = torch.tensor([61, 1, 40], dtype=torch.int32)
+    out0 = torch.full((R, P, C), 3.0, dtype=dtype)
+    x = big[:, :, off:off + C]
+    y64, s64, tol = ref.conv(x.contiguous(), w, b, st, lens, True, out0)
+    y, s = ola.conv(big.cuda()[:, :, off:off + C], w.cuda(), b.cuda(), state=st.cuda(),
+                    lens=lens.cuda(), out=out0.cuda())
+    close(y, y64, tol, "y")
+    assert torch.equal(s.cpu().double(), s64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,P,H,G,dk,dv,opt", [s[1:] for s in SCAN if s[0] == BF])
+def test_scan_rows_off_16_bytes(R, P, H, G, dk, dv, opt):
+    """bf16 rows that start off a 16-byte boundary run token by token in fp32: the definition within
+    the bounds of fp32 sums."""
+    c, o = _scan_case(BF, R, P, H, G, dk, dv, **opt)
+    sp = opt.get("softplus", True)
+    out0 = torch.full((R, P, H, dv), 3.0, dtype=BF)
+    y64, S64, ty, tS = ref.scan(**c, D=o["D"], dt_bias=o["dt_bias"], z=o["z"], S_in=o["S_in"],
+                                lens=o["lens"], use_softplus=sp, out0=out0, chunked=False)
+
+    def odd(t):
+        if t is None:
+            return None
+        room = torch.zeros(t.numel() + 8, device="cuda", dtype=BF)
+        x = room[1:1 + t.numel()].view(t.shape)
+        assert x.data_ptr() % 16 == 2
+        return x.copy_(t)
+
+    cg = {n: odd(t) if n in ("v", "k", "q") else t.cuda() for n, t in c.items()}
+    y, S = ola.scan(**cg, D=cu(o["D"]), dt_bias=cu(o["dt_bias"]), z=odd(o["z"]), S_in=cu(o["S_in"]),
+                    lens=cu(o["lens"]), softplus=sp, out=odd(out0))
+    assert ola.layer_status() == ola.OLA_OK
+    close(y, y64, ty, "y")
+    close(S, S64, tS, "state")
