@@ -351,9 +351,10 @@ ola_status ola_qk_norm(const ola_qk_desc* d, const void* q, const void* k, const
  *   ws      : device scratch of ola_scan_workspace_bytes(d) bytes, 16-byte aligned (NULL if 0).
  *             Calls that may overlap on the GPU need scratch of their own.
  * d_k, d_v in {16, 32, 64, 128, 256}, G divides H, R * H <= 2^24, P 0..2^30. dt * A is taken to
- * be <= 0 (a decay); growth is computed as the formula says as long as it does not overflow. A NaN
- * or infinity reaches what the formula makes of it and no earlier token, row or column. States and sums are
- * fp32. bf16 prompts with 16-byte aligned rows and d_k <= 128 run in chunks of 128 tokens on
+ * be <= 0 (a decay); growth is computed as the formula says as long as no product of the decays of
+ * a call overflows. A NaN or infinity makes not finite what the formula makes so and no earlier token,
+ * other row or column; where the formula gives an infinity, the result may be a NaN. States and sums
+ * are fp32. bf16 prompts with 16-byte aligned rows and d_k <= 128 run in chunks of 128 tokens on
  * tensor cores: keys, queries and v enter exactly; the token-to-token weights and the copy of
  * the state that meets the queries are rounded to bf16 on the way to y (y itself is bf16), the
  * products that build the state are not (S_out is good to fp32). Everything else runs token by
@@ -374,7 +375,9 @@ ola_status ola_scan(const ola_scan_desc* d, const void* v, const float* dt, cons
 /* ola_scan for one token of each of B = d->P beams per request: v, z, y [R][B][H][d_v],
  * k, q [R][B][G][d_k], dt [R][B][H], state_in [R][Bp][H][d_v][d_k] fp32, state_out
  * [R][B][H][d_v][d_k] fp32 (required; state_in itself if parent_idx is NULL and Bp = B).
- * States 16-byte aligned. Token by token in fp32. Errors as ola_scan. */
+ * States 16-byte aligned. Token by token in fp32. Every beam's state is materialised, as on the
+ * FullState path of the decoder: its memory and traffic grow with B * H * d_v * d_k. Errors as
+ * ola_scan. */
 ola_status ola_scan_step(const ola_scan_desc* d, int32_t Bp, const void* v, const float* dt,
                          const float* A, const void* k, const void* q, const float* D,
                          const float* dt_bias, const void* z, const float* state_in,

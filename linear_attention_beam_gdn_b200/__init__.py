@@ -727,7 +727,9 @@ def scan(v, dt, A, k, q, *, D=None, dt_bias=None, z=None, S_in=None, lens=None, 
     (bf16 or fp32, may be column slices), dt [R, P, H] fp32, A [H] fp32 (negative), optional D,
     dt_bias [H] fp32, gate z like v, S_in [R, H, d_v, d_k] fp32, lens [R] int32.
     Returns (y [R, P, H, d_v], S_out [R, H, d_v, d_k]); rows of `out` behind a sequence's end are
-    not written. S_out may be S_in."""
+    not written. S_out may be S_in. bf16 with 16-byte aligned rows and d_k <= 128 runs in chunks on
+    tensor cores: y's token-to-token weights and the copy of the state that meets the queries are
+    rounded to bf16 on the way (S_out is not). fp32 tensors keep everything in fp32."""
     torch = _torch()
     ix, code = _first(v, "v", 4)
     R, P, H, d_v = vs = v.shape
@@ -757,7 +759,8 @@ def scan_step(v, dt, A, k, q, *, state, D=None, dt_bias=None, z=None, parent_idx
     """One token of every beam through the scan (ola_scan_step): v [R, B, H, d_v], k, q
     [R, B, G, d_k], dt [R, B, H], state [R, Bp, H, d_v, d_k] fp32, parent_idx [R, B] int32
     (default: beam b continues state b, or the only one). Returns (y [R, B, H, d_v], state_out
-    [R, B, H, d_v, d_k]); state_out may be `state` when parent_idx is None."""
+    [R, B, H, d_v, d_k]); state_out may be `state` when parent_idx is None. Every beam's state is
+    materialised: its memory and traffic grow with the beams."""
     torch = _torch()
     ix, code = _first(v, "v", 4)
     R, B, H, d_v = vs = v.shape

@@ -13,9 +13,10 @@
 // Loads run through a ring in shared memory that each thread fills for itself (cp.async): deep
 // prefetch without registers or barriers. Measured: 8 x 5120 tokens of 6144 bf16 channels in 167 us
 // (1.0 GB, 92 % of the copy rate; before the ring 244 us, with 8-byte vectors 270); 8192 beams in
-// 112 us (91 %; without the ring 135 us). One prompt of 1024 tokens takes 8.3 us where the copy
-// rate gives 3.9: launch, taps and the ring's first fill. Rows whose start or
-// stride is not a multiple of 16 bytes go one channel per thread.
+// 112 us (91 %; without the ring 135 us). One prompt of 1024 tokens takes 10.5 us from HBM (8.3 out
+// of L2) where the copy rate gives 3.9: launch, taps and the ring's first fill. Rows whose start or
+// stride is not a multiple of 16 bytes go one channel per thread, without the ring: 4 x 2000 tokens of
+// 1001 bf16 channels in 19.3 us, where the copy rate gives 4.9.
 #include <type_traits>
 
 #include "ola_layer.cuh"
@@ -371,8 +372,12 @@ cudaError_t launch(ConvArgs a, int in_dtype, int W, bool wide, bool step, cudaSt
   // Tokens (beams) per thread: the count whose waves of blocks, two per SM, end first. A wave takes
   // its count and a start (taps, window, the ring's first fill) worth 8 tokens, or a beam. Against
   // powers of two that leave 1 (prompts) or 8 blocks for every SM: 1 x 1024 tokens of 6144 channels
-  // 8.3 us and 9.7, 4 x 1024 22 and 25, 8 x 5120 167 and 177, 1024 beams 18 and 26, 8192 beams 112
-  // both. Longer stretches: prompts up to 256 173 us (of 167), beams up to 16 114 (of 112).
+  // 8.3 us and 9.7 (out of L2), 4 x 1024 22 and 25, 8 x 5120 167 and 177, 1024 beams 18 and 26, 8192
+  // beams 112 both. Longer stretches: prompts up to 256 173 us (of 167), beams up to 16 114 (of 112).
+  // Two per SM is what the 16-byte kernels' registers and ring leave room for; the single-channel
+  // kernels would hold more and follow the same rule unmeasured. Stretches do not span sequences:
+  // many sequences of a few tokens leave most thread rows idle (1024 x 4 tokens of 6144: 273 us, floor
+  // 21).
   const int64_t slots = 2 * int64_t(sms);
   int64_t least = 0;
   for (int tt = step ? 2 : 4; tt <= (step ? 12 : 64); tt += step ? 1 : 4) {

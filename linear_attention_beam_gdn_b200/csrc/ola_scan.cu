@@ -7,7 +7,7 @@
 // eight partial sums of o are joined by shuffles, those of four tokens together. Tokens are staged
 // in shared memory 16 at a time as they are, the next tile's copies in flight while one is worked
 // on; what bounds it is the arithmetic, three packed operations per two state elements and token,
-// and their latency where few blocks run (8 x 792 tokens of 16 heads of 64 x 128 in fp32: 204 us, the
+// and their latency where few blocks run (8 x 792 tokens of 16 heads of 64 x 128 in fp32: 200 us, the
 // operations alone 69 us, the bytes 24).
 //
 // A long prompt of few sequences is cut into pieces: a first pass leaves each piece's own state

@@ -34,14 +34,16 @@
 // alone first (FULL = false), then, once scan_join_kernel has made the state before every piece,
 // the outputs.
 //
-// What bounds it: not HBM (64 prompts of 5120 tokens, 16 heads of 128 x 128: 5.5 GB in 1.57 ms of
-// short runs, 53 % of the copy rate; 46 % in long ones, where the clock falls) and not the matrix
-// pipe (36 % busy), but shared memory: every chunk passes 16 KB of v, y, three parts of W V and the
-// keys and queries through it, most of it twice, and its data pipe is at 70 % with the chains above
-// in front of two stages (64 KB of keys and queries each, three would not fit). Measured and worse:
-// y stored straight from registers (1.74 ms), y staged over the queries (1.90), P in place of G
-// behind barriers of 64 threads (1.74), 16 state columns at a time (1.63), four W V or four output
-// warps (1.85 against 1.79 in long runs).
+// What bounds it: not HBM (64 prompts of 5120 tokens, 16 heads of 128 x 128: 5.5 GB in 1.60 ms of
+// short runs, 52 % of the copy rate; 1.91-1.96 ms in long ones, where the clock falls), not the matrix
+// pipe (32 % busy) and not shared memory alone, though every chunk passes 16 KB of v, y, three parts
+// of W V and the keys and queries through it, most of it twice (60 % of its data pipe): the chains
+// above stand in front of two stages (64 KB of keys and queries each, three would not fit). The wait
+// of G for the read of P is part of them: 1.60 ms with it, 1.57 in the order of issue alone, which
+// nothing guarantees. Measured before that wait, and worse than 1.54-1.57 ms: y stored straight from
+// registers (1.74 ms), y staged over the queries (1.90), P in place of G behind barriers of 64 threads
+// (1.74), 16 state columns at a time (1.63), four W V or four output warps (1.85 against 1.79 in long
+// runs).
 #include "ola_layer.cuh"
 
 namespace ola {
