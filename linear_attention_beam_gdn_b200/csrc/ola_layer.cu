@@ -9,7 +9,8 @@
 
 using namespace ola;
 
-// code, detail, index of the first error recorded since it was last read (see report_error)
+// The code of the first error recorded since it was last read, which ola_layer_status returns; its
+// detail and index (see report_error) lie beside it for a debugger.
 static __device__ int g_layer_err[4];
 // what status calls took from it, a slot for each call under way
 constexpr int kTaken = 1024;
